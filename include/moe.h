@@ -1,6 +1,7 @@
 /*
  * libmoe -- forward pass of a DeepSeek-V3 / DeepSeek-V2-Lite mixture-of-experts
- * layer on one NVIDIA B200 (sm_100a).
+ * layer on one NVIDIA B200 (sm_100a), and the backward pass of its experts and
+ * router.
  *
  * The layer, as the pages state it:
  *   [MoE-walk]    zhiyuanblog.org "MoE 混合专家模型推理参数与前向传播详解":
@@ -375,6 +376,80 @@ MOE_API moe_status moe_gate_up_swiglu_gather(int32_t rows, int32_t H, const moe_
                                      const void* x, int32_t T, const int32_t* src_token,
                                      const int32_t* offsets, void* h_ws,
                                      int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * Training: the experts' forward that keeps what its backward pass needs, and
+ * that backward pass ([MoE-walk] §3.3 gives the forward; the gradients are its
+ * derivative).
+ *
+ * moe_gate_up_swiglu_train: moe_gate_up_swiglu that also stores the
+ *   pre-activations. h [rows, I] bf16 = SiLU(g) * u from the fp32 sums, and
+ *   gu [rows, 2I] bf16 = [g | u] = a w13^T rounded once. bf16 weights, row-
+ *   major or tiled (MOE_ERR_UNSUPPORTED otherwise); limits of
+ *   moe_gate_up_swiglu.
+ *
+ * moe_swiglu_ffn_backward: gradients of out = row_w * (h w2^T), h = SiLU(g) * u
+ *   with [g | u] = a w13^T, at the saved pre-activations:
+ *     dh0     = d_out w2                       d_row_w[r] = sum_i h[r,i] dh0[r,i]
+ *     dh      = row_w * dh0
+ *     dg      = dh u s (1 + g (1 - s)),  du = dh g s,    s = sigmoid(g)
+ *     d_a     = [dg | du] w13
+ *     d_w13[e] = [dg | du]^T a  and  d_w2[e] = d_out^T (row_w h)  over segment e
+ *   a       [rows, H] bf16 the forward's rows (may be NULL without d_w13)
+ *   gu      [rows, 2I] bf16 from moe_gate_up_swiglu_train
+ *   d_out   [rows, H] bf16 gradient of out (moe_permute of the gradient of y
+ *           gives it for the whole layer)
+ *   offsets, row_w  as in the forward (row_w NULL = 1)
+ *   w       bf16 weights, row-major or tiled; w13 may be NULL without d_a
+ *   d_a     [rows, H] bf16;  d_row_w [rows] fp32
+ *   d_w13   [groups, 2I, H], d_w2 [groups, H, I], both row-major (also for
+ *           tiled weights), bf16 or fp32 by grad_dtype. accumulate = 1
+ *           (MOE_F32 only) adds to what is there; otherwise an expert without
+ *           rows gets zeros.
+ *   Any output may be NULL (not computed), but not all of them. Rows outside
+ *   [offsets[0], offsets[groups]) are not read and their outputs are left as
+ *   they were.
+ *   workspace  device scratch of moe_swiglu_ffn_backward_workspace_size()
+ *           bytes (dg and du, row_w * h, partial sums); calls in flight at
+ *           once need one each.
+ *   dh0 and the activation's derivative are fp32; dg, du and row_w * h are
+ *   rounded to bf16 once, as the operands of the second products; every sum
+ *   is fp32 in a fixed order, so results do not vary from run to run.
+ *   A segment of offsets outside [0, rows] is cut to it and flagged
+ *   MOE_DEVSTAT_BAD_EXPERT_ID in dev_status.
+ *
+ * moe_route_backward: gradient of the routing weights w.r.t. the logits:
+ *     w_j = scale s_j (/ sum_i s_i with norm_topk_prob), s the softmax or
+ *     sigmoid scores of the token's k chosen experts. The selection, its bias
+ *     and its groups have no gradient.
+ *   logits [T, E] fp32, topk_ids [T, k] from moe_route (ids of -1 are skipped,
+ *   ids >= E skipped and flagged); d_topk_w [T*k] fp32 in slot order, or, with
+ *   slot_to_row [T*k] (moe_permute), in row order (d_row_w as above; a row
+ *   outside [0, T*k) counts as 0 and is flagged).
+ *   d_logits [T, E] fp32 out; d_logits_bf16 [T, E] out or NULL: the same,
+ *   rounded, for moe_gate_backward. Limits of moe_route.
+ *
+ * moe_gate_backward: gradients of the gate projection logits = x gate^T:
+ *     dx = dx_in + d_logits gate   (bf16; dx_in NULL = 0, and may be dx)
+ *     d_gate = d_logits^T x        (bf16 or fp32, accumulate, as above)
+ *   d_logits_bf16 [T, E]; x [T, H]; gate_w [E, H]; dx or d_gate may be NULL.
+ *   Limits: H % 256 == 0, E % 16 == 0, 16 <= E <= 256.
+ * ------------------------------------------------------------------------ */
+MOE_API moe_status moe_gate_up_swiglu_train(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* a,
+                              const int32_t* offsets, void* h, void* gu, int32_t* dev_status, void* stream);
+MOE_API moe_status moe_swiglu_ffn_backward_workspace_size(int32_t rows, int32_t I, size_t* bytes);
+MOE_API moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* a,
+                              const void* gu, const void* d_out, const int32_t* offsets, const float* row_w,
+                              void* d_a, void* d_w13, void* d_w2, moe_dtype grad_dtype, int32_t accumulate,
+                              float* d_row_w, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream);
+MOE_API moe_status moe_route_backward(int32_t T, int32_t E, int32_t k, moe_scoring scoring, int32_t norm_topk_prob,
+                              float routed_scaling_factor, const float* logits, const int32_t* topk_ids,
+                              const float* d_topk_w, const int32_t* slot_to_row, float* d_logits,
+                              void* d_logits_bf16, int32_t* dev_status, void* stream);
+MOE_API moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logits_bf16, const void* x,
+                              const void* gate_w, const void* dx_in, void* dx, void* d_gate, moe_dtype grad_dtype,
+                              int32_t accumulate, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ *
  * moe_combine -- unpermute and weighted combine, [MoE-walk] §3.4:

@@ -4,7 +4,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "kernels.cuh"
+#include "train.cuh"
 
 
 using namespace moe;
@@ -430,6 +430,37 @@ moe_status moe_gate_up_swiglu_gather(int32_t rows, int32_t H, const moe_ffn_weig
   return check_launch(launch_grouped_gemm(false, EPI_SWIGLU, tmA, tmB, g1, nsm, as_stream(stream)));
 }
 
+moe_status moe_gate_up_swiglu_train(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* a,
+                                    const int32_t* offsets, void* h, void* gu, int32_t* dev_status, void* stream) {
+  moe_status s = check_ffn(rows, H, w, a, nullptr, true, false);
+  if (s != MOE_OK) return s;
+  if (w->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!h || !gu || (!offsets && w->groups != 1)) return MOE_ERR_INVALID_ARG;
+  if (any_misaligned(offsets, h, gu)) return MOE_ERR_ALIGNMENT;
+  int nsm = 0;
+  if ((s = sm_count(&nsm)) != MOE_OK) return s;
+  const int I = w->I;
+  CUtensorMap tmA;
+  TokenMaps tmB;
+  s = w->tiled ? make_tmap(&tmA, w->w13, false, 64, static_cast<uint64_t>(w->groups) * 2 * I * (H / 64), 256)
+               : make_tmap(&tmA, w->w13, false, H, static_cast<uint64_t>(w->groups) * 2 * I, 128);
+  if (s != MOE_OK) return s;
+  if ((s = make_token_tmaps(&tmB, a, false, H, rows)) != MOE_OK) return s;
+  TrainGemmArgs g;
+  g.rows = rows;
+  g.K = H;
+  g.M = I;
+  g.groups = w->groups;
+  g.offsets = offsets;
+  g.n_mblk = I / 128;
+  g.tiled = w->tiled;
+  g.gu = static_cast<__nv_bfloat16*>(gu);
+  g.h = static_cast<__nv_bfloat16*>(h);
+  g.status = dev_status;
+  g.wait_ns = wait_limit();
+  return check_launch(launch_train_gemm(TRAIN_FORWARD, tmA, tmB, g, nsm, as_stream(stream)));
+}
+
 moe_status moe_down_proj(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* h, const float* h_scale,
                          const int32_t* offsets, const float* row_w, void* out, int32_t* dev_status,
                          void* stream) {
@@ -664,6 +695,219 @@ moe_status moe_read_device_status(const int32_t* dev_status, int32_t* out, void*
   if (v == 0) return MOE_OK;
   if (v == MOE_DEVSTAT_TIMEOUT) return MOE_ERR_DEVICE_TIMEOUT;
   return MOE_ERR_DEVICE_CHECK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// [outer, inner] matrix stored through boxes of box_rows rows x 128 bytes,
+// bf16 or fp32.
+moe_status make_out_tmap(CUtensorMap* m, const void* ptr, bool f32, uint64_t inner, uint64_t outer, uint32_t box_rows) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
+  const uint64_t esize = f32 ? 4 : 2;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner * esize};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
+  return MOE_OK;
+}
+
+size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// Parts of moe_swiglu_ffn_backward's workspace.
+struct BackwardWs {
+  size_t d_gu, hw, partial, total;
+};
+BackwardWs backward_ws(int32_t rows, int32_t I) {
+  BackwardWs b;
+  const size_t r = static_cast<size_t>(rows);
+  b.d_gu = 0;
+  b.hw = align256(r * 2 * I * 2);
+  b.partial = b.hw + align256(r * I * 2);
+  b.total = b.partial + align256(r * (I / 32) * 4);
+  return b;
+}
+
+// One weight-gradient product: C[g] [M, N] from A [rows, M] and B [rows, N].
+moe_status plan_wgrad(WgradProblem* p, int32_t rows, int32_t groups, const void* A, int32_t M, const void* B, int32_t N,
+                      void* out, bool f32, int subs) {
+  moe_status s = make_tmap(&p->tmA, A, false, M, rows, 64);
+  if (s != MOE_OK) return s;
+  if ((s = make_tmap(&p->tmB, B, false, N, rows, 64)) != MOE_OK) return s;
+  if ((s = make_out_tmap(&p->tmOut, out, f32, N, static_cast<uint64_t>(groups) * M, 32)) != MOE_OK) return s;
+  p->M = M;
+  p->N = N;
+  p->tiles = groups * ((M + 128 * subs - 1) / (128 * subs)) * ((N + 255) / 256);
+  return MOE_OK;
+}
+
+// Features per wgrad tile (in units of 128): see wgrad_kernel.
+int wgrad_subs(int32_t rows, int32_t groups) { return rows / groups >= 512 ? 2 : 1; }
+
+bool grad_args_ok(moe_dtype grad_dtype, int32_t accumulate) {
+  if (grad_dtype != MOE_BF16 && grad_dtype != MOE_F32) return false;
+  return accumulate == 0 || (accumulate == 1 && grad_dtype == MOE_F32);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_swiglu_ffn_backward_workspace_size(int32_t rows, int32_t I, size_t* bytes) {
+  if (!bytes || rows < 1 || I < 1) return MOE_ERR_INVALID_ARG;
+  if (I % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  *bytes = backward_ws(rows, I).total;
+  return MOE_OK;
+}
+
+moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* a, const void* gu,
+                                   const void* d_out, const int32_t* offsets, const float* row_w, void* d_a,
+                                   void* d_w13, void* d_w2, moe_dtype grad_dtype, int32_t accumulate, float* d_row_w,
+                                   void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  moe_status s = check_ffn(rows, H, w, d_out, nullptr, d_a != nullptr, true);
+  if (s != MOE_OK) return s;
+  if (w->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!gu || !workspace || (d_w13 && !a) || (!offsets && w->groups != 1)) return MOE_ERR_INVALID_ARG;
+  if (!d_a && !d_w13 && !d_w2 && !d_row_w) return MOE_ERR_INVALID_ARG;
+  if (!grad_args_ok(grad_dtype, accumulate)) return MOE_ERR_INVALID_ARG;
+  const BackwardWs ws = backward_ws(rows, w->I);
+  if (workspace_bytes < ws.total) return MOE_ERR_INVALID_ARG;
+  if (any_misaligned(a, gu, d_out, offsets, row_w, d_a, d_w13, d_w2, d_row_w, workspace)) return MOE_ERR_ALIGNMENT;
+  const int32_t I = w->I;
+  // output tiles of the weight gradients are counted in int32
+  if (static_cast<long long>(w->groups) * (2 * I / 128) * (H / 256) > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED;
+  int nsm = 0;
+  if ((s = sm_count(&nsm)) != MOE_OK) return s;
+  cudaStream_t st = as_stream(stream);
+  char* base = static_cast<char*>(workspace);
+  void* d_gu = base + ws.d_gu;
+  void* hw = base + ws.hw;
+  float* partial = reinterpret_cast<float*>(base + ws.partial);
+
+  // dh0 = d_out w2 and the activation's backward: d_gu, row_w * h, partial sums of d_row_w
+  CUtensorMap tmA;
+  TokenMaps tmB;
+  s = w->tiled ? make_tmap(&tmA, w->w2, false, 64, static_cast<uint64_t>(w->groups) * H * (I / 64), 64)
+               : make_tmap(&tmA, w->w2, false, I, static_cast<uint64_t>(w->groups) * H, 64);
+  if (s != MOE_OK) return s;
+  if ((s = make_token_tmaps(&tmB, d_out, false, H, rows)) != MOE_OK) return s;
+  TrainGemmArgs g;
+  g.rows = rows;
+  g.K = H;
+  g.M = I;
+  g.groups = w->groups;
+  g.offsets = offsets;
+  g.n_mblk = (I + 255) / 256;
+  g.tiled = w->tiled;
+  g.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));   // read only
+  g.row_w = row_w;
+  g.d_gu = static_cast<__nv_bfloat16*>(d_gu);
+  g.h = static_cast<__nv_bfloat16*>(hw);
+  g.partial = partial;
+  g.status = dev_status;
+  g.wait_ns = wait_limit();
+  if ((s = check_launch(launch_train_gemm(TRAIN_HIDDEN, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
+  if (d_row_w) {
+    s = check_launch(launch_row_w_grad(rows, I / 32, partial, offsets, w->groups, d_row_w, st));
+    if (s != MOE_OK) return s;
+  }
+  if (d_a) {                                           // d_a = d_gu w13
+    s = w->tiled ? make_tmap(&tmA, w->w13, false, 64, static_cast<uint64_t>(w->groups) * 2 * I * (H / 64), 64)
+                 : make_tmap(&tmA, w->w13, false, H, static_cast<uint64_t>(w->groups) * 2 * I, 64);
+    if (s != MOE_OK) return s;
+    if ((s = make_token_tmaps(&tmB, d_gu, false, 2 * static_cast<uint64_t>(I), rows)) != MOE_OK) return s;
+    g.K = 2 * I;
+    g.M = H;
+    g.n_mblk = H / 256;
+    g.out = static_cast<__nv_bfloat16*>(d_a);
+    if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
+  }
+  if (d_w13 || d_w2) {
+    const int subs = wgrad_subs(rows, w->groups);
+    WgradArgs q{};
+    const bool f32 = grad_dtype == MOE_F32;
+    if (d_w13) {
+      s = plan_wgrad(&q.prob[q.n_prob++], rows, w->groups, d_gu, 2 * I, a, H, d_w13, f32, subs);
+      if (s != MOE_OK) return s;
+    }
+    if (d_w2) {
+      s = plan_wgrad(&q.prob[q.n_prob++], rows, w->groups, d_out, H, hw, I, d_w2, f32, subs);
+      if (s != MOE_OK) return s;
+    }
+    q.rows = rows;
+    q.groups = w->groups;
+    q.offsets = offsets;
+    q.f32 = f32;
+    q.accumulate = accumulate;
+    q.status = dev_status;
+    q.wait_ns = wait_limit();
+    s = check_launch(launch_wgrad(subs, q, nsm, st));
+  }
+  return s;
+}
+
+moe_status moe_route_backward(int32_t T, int32_t E, int32_t k, moe_scoring scoring, int32_t norm_topk_prob,
+                              float routed_scaling_factor, const float* logits, const int32_t* topk_ids,
+                              const float* d_topk_w, const int32_t* slot_to_row, float* d_logits, void* d_logits_bf16,
+                              int32_t* dev_status, void* stream) {
+  if (T < 1 || E < 1 || k < 1 || k > E || !logits || !topk_ids || !d_topk_w || !d_logits) return MOE_ERR_INVALID_ARG;
+  if (scoring != MOE_SOFTMAX && scoring != MOE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (k > 16 || E > 256 || E < 16 || E % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * k > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  if (any_misaligned(logits, topk_ids, d_topk_w, slot_to_row, d_logits, d_logits_bf16)) return MOE_ERR_ALIGNMENT;
+  return check_launch(launch_route_backward(T, E, k, scoring, norm_topk_prob ? 1 : 0, routed_scaling_factor, logits,
+                                            topk_ids, d_topk_w, slot_to_row, d_logits, d_logits_bf16, dev_status,
+                                            as_stream(stream)));
+}
+
+moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logits_bf16, const void* x,
+                             const void* gate_w, const void* dx_in, void* dx, void* d_gate, moe_dtype grad_dtype,
+                             int32_t accumulate, int32_t* dev_status, void* stream) {
+  if (T < 1 || H < 1 || E < 1 || !d_logits_bf16 || (!dx && !d_gate)) return MOE_ERR_INVALID_ARG;
+  if ((dx && !gate_w) || (d_gate && !x) || (dx_in && !dx)) return MOE_ERR_INVALID_ARG;
+  if (!grad_args_ok(grad_dtype, accumulate)) return MOE_ERR_INVALID_ARG;
+  if (H % 256 != 0 || E > 256 || E < 16 || E % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (any_misaligned(d_logits_bf16, x, gate_w, dx_in, dx, d_gate)) return MOE_ERR_ALIGNMENT;
+  int nsm = 0;
+  moe_status s = sm_count(&nsm);
+  if (s != MOE_OK) return s;
+  cudaStream_t st = as_stream(stream);
+  if (dx) {                                            // dx = dx_in + d_logits gate
+    CUtensorMap tmA;
+    TokenMaps tmB;
+    if ((s = make_tmap(&tmA, gate_w, false, H, E, 64)) != MOE_OK) return s;
+    if ((s = make_token_tmaps(&tmB, d_logits_bf16, false, E, T)) != MOE_OK) return s;
+    TrainGemmArgs g;
+    g.rows = T;
+    g.K = E;
+    g.M = H;
+    g.n_mblk = H / 256;
+    g.out = static_cast<__nv_bfloat16*>(dx);
+    g.add = static_cast<const __nv_bfloat16*>(dx_in);
+    g.status = dev_status;
+    g.wait_ns = wait_limit();
+    if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
+  }
+  if (d_gate) {                                        // d_gate = d_logits^T x
+    WgradArgs q{};
+    if ((s = plan_wgrad(&q.prob[0], T, 1, d_logits_bf16, E, x, H, d_gate, grad_dtype == MOE_F32, 1)) != MOE_OK) return s;
+    q.n_prob = 1;
+    q.rows = T;
+    q.groups = 1;
+    q.f32 = grad_dtype == MOE_F32;
+    q.accumulate = accumulate;
+    q.status = dev_status;
+    q.wait_ns = wait_limit();
+    s = check_launch(launch_wgrad(1, q, nsm, st));
+  }
+  return s;
 }
 
 }  // extern "C"

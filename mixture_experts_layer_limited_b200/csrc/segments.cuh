@@ -1,0 +1,154 @@
+// The tile schedule over expert segments and the tile loads and stores shared
+// by the training and the 4-bit grouped GEMM kernels. Tiles are (expert g,
+// feature block mb, row block tb), at most bn_max rows each, as in the forward
+// GEMMs; a segment that does not lie in the rows is cut to them and flagged.
+#pragma once
+
+#include "train.cuh"
+
+namespace moe {
+
+constexpr int kMaxGroups = 512;
+
+struct SegTile {
+  int g, mb, row0, n_valid, N;
+  int ntb;              // token blocks of this segment
+  int tb;               // this tile's token block in the segment
+};
+
+// Token blocks per rasterisation chunk: inside a segment, tiles run in chunks
+// of up to kTbChunk token blocks x all weight blocks, token block innermost,
+// so CTAs running side by side share the weight block (HBM once, then L2)
+// and the chunk's token blocks (L2).
+constexpr int kTbChunk = 8;
+
+// A grouped GEMM as the schedule sees it.
+struct SegProblem {
+  int32_t rows, groups;
+  const int32_t* offsets;   // [groups + 1] or nullptr (one segment of all rows)
+  int32_t n_mblk;           // feature blocks per group
+  int32_t bn_max;           // max rows per tile (multiple of 32, <= 256)
+  int32_t* status;
+};
+
+// Per-CTA copy of the tile schedule: each group's first tile and first row.
+struct SegSched {
+  int tile_start[kMaxGroups + 1];
+  int seg_start[kMaxGroups + 1];
+};
+
+__device__ __forceinline__ int tiles_of(int n, int bn_max, int n_mblk) {
+  return n <= 0 ? 0 : ((n + bn_max - 1) / bn_max) * n_mblk;
+}
+
+// Warp-cooperative build of the schedule (called by one warp).
+__device__ __forceinline__ void build_schedule(SegSched& s, const SegProblem& a, int lane) {
+  int carry = 0;
+  for (int base = 0; base < a.groups; base += 32) {
+    const int g = base + lane;
+    int st = 0, n = 0;
+    if (g < a.groups) {
+      if (a.offsets) {
+        st = a.offsets[g];
+        int end = a.offsets[g + 1];
+        if (st < 0 || end < st || end > a.rows) {       // a segment outside the rows: flagged, cut to them
+          flag_status(a.status, MOE_DEVSTAT_BAD_EXPERT_ID);
+          st = min(max(st, 0), a.rows);
+          end = min(max(end, st), a.rows);
+        }
+        n = end - st;
+      } else {
+        st = 0;
+        n = a.rows;
+      }
+    }
+    int t = (g < a.groups) ? tiles_of(n, a.bn_max, 1) : 0;   // token blocks
+    int incl = t;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (g < a.groups) {
+      s.tile_start[g] = (carry + incl - t) * a.n_mblk;
+      s.seg_start[g] = st;
+    }
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) {
+    s.tile_start[a.groups] = carry * a.n_mblk;
+    s.seg_start[a.groups] = a.offsets ? min(max(a.offsets[a.groups], 0), a.rows) : a.rows;
+  }
+}
+
+// Tile `local` of a segment of n rows starting at row seg0 (group g).
+__device__ __forceinline__ SegTile decode_in_segment(const SegProblem& a, int g, int seg0, int n, int local) {
+  SegTile ti;
+  ti.g = g;
+  const int ntb = (n + a.bn_max - 1) / a.bn_max;
+  const int bn = ((((n + ntb - 1) / ntb) + 15) / 16) * 16;
+  const int chunk_tiles = kTbChunk * a.n_mblk;
+  const int chunk = local / chunk_tiles;
+  const int r = local - chunk * chunk_tiles;
+  const int c_tb = min(kTbChunk, ntb - chunk * kTbChunk);   // token blocks in this chunk
+  ti.mb = r / c_tb;
+  const int tb = chunk * kTbChunk + (r - ti.mb * c_tb);
+  ti.ntb = ntb;
+  ti.tb = tb;
+  ti.row0 = seg0 + tb * bn;
+  ti.n_valid = min(bn, n - tb * bn);
+  ti.N = ((ti.n_valid + 15) / 16) * 16;
+  return ti;
+}
+
+__device__ __forceinline__ SegTile decode_tile(const SegSched& s, const SegProblem& a, int t) {
+  int lo = 0, hi = a.groups - 1;   // last g with tile_start[g] <= t
+  while (lo < hi) {
+    int mid = (lo + hi + 1) >> 1;
+    if (s.tile_start[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return decode_in_segment(a, lo, s.seg_start[lo], s.seg_start[lo + 1] - s.seg_start[lo],
+                           t - s.tile_start[lo]);
+}
+
+// Token rows of one stage (a multiple of 16, at most 256) are fetched with at
+// most one box of each size 256, 128, 64, 32, 16: the binary digits of
+// rows / 16. Returns rows loaded.
+template <typename LoadFn>
+__device__ __forceinline__ int load_token_rows(int rows, LoadFn&& load) {
+  int off = 0;
+#pragma unroll
+  for (int i = 0; i < kTokBoxes; ++i) {
+    const int box = 256 >> i;
+    if (rows - off >= box) { load(i, off); off += box; }
+  }
+  return off;
+}
+
+// Writes NT tokens x 32 features (thread = feature lane, v[j] = token j) to
+// out[(row0 + j) * ld + feat0 + lane] through a per-warp shared tile, so that
+// every global store is a 16-byte vector (4 lanes cover one token's 32
+// features). Tokens j >= n_rows are not written.
+template <int NT>
+__device__ __forceinline__ void store_tile(__nv_bfloat16* stage, const float (&v)[NT], int lane,
+                                           __nv_bfloat16* out, size_t ld, int row0, int n_rows, int feat0) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j) stage[j * 32 + lane] = __float2bfloat16_rn(v[j]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < NT / 8; ++i) {
+    const int t = (lane >> 2) + 8 * i;
+    const int seg = lane & 3;
+    if (t < n_rows) {
+      const uint4 val = *reinterpret_cast<const uint4*>(stage + t * 32 + seg * 8);
+      *reinterpret_cast<uint4*>(out + static_cast<size_t>(row0 + t) * ld + feat0 + seg * 8) = val;
+    }
+  }
+  __syncwarp();
+}
+
+// SiLU(g) = g * sigmoid(g). Fast division: for g < -88 the exponential
+// overflows to inf and the quotient is the correct limit (-0).
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+}  // namespace moe

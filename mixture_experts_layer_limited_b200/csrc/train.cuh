@@ -1,0 +1,54 @@
+// Argument blocks and launchers of the training and the 4-bit kernels.
+#pragma once
+
+#include "kernels.cuh"
+
+namespace moe {
+
+// The training GEMMs over expert segments, one tile scheme (256 weight-side
+// rows by up to 256 token rows):
+//   TRAIN_FORWARD  [g | u] = B w13^T, h = SiLU(g) * u; gu and h stored. K = H, M = I
+//   TRAIN_HIDDEN   dh0 = B w2 (B = d_out), then the activation's backward. K = H, M = I
+//   TRAIN_ROWS     out = B W (+ add), W [groups, K, M] row-major or tiled w13
+enum { TRAIN_FORWARD = 0, TRAIN_HIDDEN = 1, TRAIN_ROWS = 2 };
+struct TrainGemmArgs {
+  int32_t rows = 0, K = 0, M = 0, groups = 1;
+  const int32_t* offsets = nullptr;   // [groups + 1] or nullptr (one segment)
+  int32_t n_mblk = 0;                 // feature blocks: 128 (forward), 256 (else; the last may hold 128)
+  int32_t tiled = 0;                  // W in moe_tile_ffn_weights' layout
+  __nv_bfloat16* gu = nullptr;        // [rows, 2I]: forward out, hidden in
+  __nv_bfloat16* h = nullptr;         // [rows, I] out: forward h, hidden row_w * h
+  const float* row_w = nullptr;       // hidden: [rows] or nullptr (= 1)
+  __nv_bfloat16* d_gu = nullptr;      // hidden: [rows, 2I] out
+  float* partial = nullptr;           // hidden: [I / 32, rows] out, partial sums of d_row_w
+  __nv_bfloat16* out = nullptr;       // rows: [rows, M]
+  const __nv_bfloat16* add = nullptr; // rows: [rows, M] added to the product, or nullptr (may be `out`)
+  int32_t* status = nullptr;
+  uint64_t wait_ns = kDefaultWaitLimitNs;
+};
+cudaError_t launch_train_gemm(int mode, const CUtensorMap& tmA, const TokenMaps& tmB, const TrainGemmArgs& a, int grid,
+                              cudaStream_t stream);
+cudaError_t launch_row_w_grad(int rows, int n, const float* partial, const int32_t* offsets, int groups, float* d_row_w,
+                              cudaStream_t stream);
+
+// Weight gradients C[g] [M, N] = A[rows of g]^T B[rows of g]; up to two such
+// products over the same segments in one launch.
+struct WgradProblem {
+  CUtensorMap tmA, tmB;               // [rows, M], [rows, N] bf16, boxes of 64 rows x 64 columns
+  CUtensorMap tmOut;                  // [groups * M, N], boxes of 32 rows x 128 bytes
+  int32_t M, N, tiles;
+};
+struct WgradArgs {
+  WgradProblem prob[2];
+  int32_t n_prob, rows, groups;
+  const int32_t* offsets;
+  int32_t f32, accumulate;            // output type; fp32 only: add to what is there
+  int32_t* status;
+  uint64_t wait_ns;
+};
+cudaError_t launch_wgrad(int subs, const WgradArgs& a, int grid, cudaStream_t stream);
+cudaError_t launch_route_backward(int T, int E, int k, int scoring, int norm, float scale, const float* logits,
+                                  const int32_t* ids, const float* d_w, const int32_t* slot_to_row, float* d_logits,
+                                  void* d_logits16, int32_t* status, cudaStream_t stream);
+
+}  // namespace moe

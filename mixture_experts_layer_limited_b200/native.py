@@ -32,6 +32,8 @@ EXPORTED = [
     "moe_gate_up_swiglu_with_shared", "moe_down_proj_with_shared", "moe_down_proj_combine",
     "moe_swiglu_ffn_sync_size", "moe_swiglu_ffn_with_shared", "moe_tile_ffn_weights",
     "moe_combine", "moe_bias_update", "moe_aux_loss_workspace_size", "moe_aux_loss",
+    "moe_gate_up_swiglu_train", "moe_swiglu_ffn_backward_workspace_size", "moe_swiglu_ffn_backward",
+    "moe_route_backward", "moe_gate_backward",
     "moe_quantize_blocks", "moe_quantize_rows",
     "moe_read_device_status", "moe_last_cuda_error", "moe_status_string", "moe_abi_version",
     "moe_set_wait_limit_ns", "moe_wait_limit_ns",
@@ -99,6 +101,12 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_bias_update": [_I, _I, _I, _P, _P, ctypes.c_float, _P, _P],
         "moe_aux_loss_workspace_size": [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)],
         "moe_aux_loss": [_I, _I, _I, _I, _I, _P, _P, ctypes.c_float, _P, _P, ctypes.c_size_t, _P, _P],
+        "moe_gate_up_swiglu_train": [_I, _I, ctypes.POINTER(FFNWeights), _P, _P, _P, _P, _P, _P],
+        "moe_swiglu_ffn_backward_workspace_size": [_I, _I, ctypes.POINTER(ctypes.c_size_t)],
+        "moe_swiglu_ffn_backward": [_I, _I, ctypes.POINTER(FFNWeights), _P, _P, _P, _P, _P, _P, _P, _P, _I, _I,
+                                    _P, _P, ctypes.c_size_t, _P, _P],
+        "moe_route_backward": [_I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P],
+        "moe_gate_backward": [_I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P],
         "moe_quantize_blocks": [_I, _I, _I, _P, _P, _P, _P],
         "moe_quantize_rows": [_I, _I, _P, _P, _P, _P],
         "moe_read_device_status": [_P, ctypes.POINTER(ctypes.c_int32), _P],
@@ -139,6 +147,19 @@ def _check(fn: str, status: int):
         if status == MOE_ERR_CUDA:
             detail += f", cuda error {lib.moe_last_cuda_error()}"
         raise MoEError(fn, status, detail)
+
+
+def _expect(fn: str, **tensors):
+    """name=(tensor or None, elements, dtype): device, type and size of a call's
+    tensors, checked before any pointer is passed on."""
+    dev = torch.cuda.current_device()
+    for name, (t, n, dtype) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype or t.numel() < n:
+            raise ValueError(f"{fn}: {name} has {t.numel()} elements of {t.dtype}, expected {n} of {dtype}")
+        if t.device.index != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{dev}")
 
 
 # ---------------------------------------------------------------- the ABI
@@ -283,6 +304,72 @@ def moe_down_proj_combine(rows, T, H, w2, groups, I, h, offsets, row_w, src_toke
         rows, T, H, ctypes.byref(w), _ptr(h), _ptr(offsets), _ptr(row_w), _ptr(src_token),
         ctypes.byref(sw) if sw is not None else None, _ptr(sh_h), _ptr(acc_ws), _ptr(y),
         _ptr(dev_status), _stream(stream)))
+
+
+def _grad(fn, grad_dtype):
+    if grad_dtype not in (MOE_BF16, MOE_F32):
+        raise ValueError(f"{fn}: gradients are MOE_BF16 or MOE_F32")
+    return torch.float32 if grad_dtype == MOE_F32 else torch.bfloat16
+
+
+def moe_gate_up_swiglu_train(rows, H, w13, groups, I, a, offsets, h, gu, dev_status=None, stream=None,
+                             tiled=False):
+    """moe_gate_up_swiglu that also stores the pre-activations gu [rows, 2I]."""
+    bf = torch.bfloat16
+    _expect("moe_gate_up_swiglu_train", w13=(w13, groups * 2 * I * H, bf), a=(a, rows * H, bf),
+            offsets=(offsets, groups + 1, torch.int32), h=(h, rows * I, bf), gu=(gu, rows * 2 * I, bf))
+    w = FFNWeights(_ptr(w13), None, None, None, MOE_BF16, groups, I)
+    w.tiled = int(tiled)
+    _check("moe_gate_up_swiglu_train", load_library().moe_gate_up_swiglu_train(
+        rows, H, ctypes.byref(w), _ptr(a), _ptr(offsets), _ptr(h), _ptr(gu), _ptr(dev_status), _stream(stream)))
+
+
+def moe_swiglu_ffn_backward_workspace_size(rows, I) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_swiglu_ffn_backward_workspace_size",
+           load_library().moe_swiglu_ffn_backward_workspace_size(rows, I, ctypes.byref(n)))
+    return n.value
+
+
+def moe_swiglu_ffn_backward(rows, H, w13, w2, groups, I, a, gu, d_out, offsets, row_w, d_a, d_w13, d_w2, d_row_w,
+                            workspace, grad_dtype=MOE_BF16, accumulate=False, dev_status=None, stream=None,
+                            tiled=False):
+    """Gradients of the experts' block at the pre-activations gu that
+    moe_gate_up_swiglu_train saved; outputs that are None are not computed."""
+    bf, f32, gt = torch.bfloat16, torch.float32, _grad("moe_swiglu_ffn_backward", grad_dtype)
+    _expect("moe_swiglu_ffn_backward", w13=(w13, groups * 2 * I * H, bf), w2=(w2, groups * H * I, bf),
+            a=(a, rows * H, bf), gu=(gu, rows * 2 * I, bf), d_out=(d_out, rows * H, bf),
+            offsets=(offsets, groups + 1, torch.int32), row_w=(row_w, rows, f32), d_a=(d_a, rows * H, bf),
+            d_w13=(d_w13, groups * 2 * I * H, gt), d_w2=(d_w2, groups * H * I, gt), d_row_w=(d_row_w, rows, f32))
+    w = FFNWeights(_ptr(w13), _ptr(w2), None, None, MOE_BF16, groups, I)
+    w.tiled = int(tiled)
+    _check("moe_swiglu_ffn_backward", load_library().moe_swiglu_ffn_backward(
+        rows, H, ctypes.byref(w), _ptr(a), _ptr(gu), _ptr(d_out), _ptr(offsets), _ptr(row_w), _ptr(d_a),
+        _ptr(d_w13), _ptr(d_w2), grad_dtype, int(bool(accumulate)), _ptr(d_row_w), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
+
+
+def moe_route_backward(T, E, k, scoring, norm_topk_prob, routed_scaling_factor, logits, topk_ids, d_topk_w,
+                       slot_to_row, d_logits, d_logits_bf16=None, dev_status=None, stream=None):
+    """d_topk_w in slot order (slot_to_row None), or in row order with it."""
+    f32, i32 = torch.float32, torch.int32
+    _expect("moe_route_backward", logits=(logits, T * E, f32), topk_ids=(topk_ids, T * k, i32),
+            d_topk_w=(d_topk_w, T * k, f32), slot_to_row=(slot_to_row, T * k, i32), d_logits=(d_logits, T * E, f32),
+            d_logits_bf16=(d_logits_bf16, T * E, torch.bfloat16))
+    _check("moe_route_backward", load_library().moe_route_backward(
+        T, E, k, scoring, int(bool(norm_topk_prob)), float(routed_scaling_factor), _ptr(logits), _ptr(topk_ids),
+        _ptr(d_topk_w), _ptr(slot_to_row), _ptr(d_logits), _ptr(d_logits_bf16), _ptr(dev_status), _stream(stream)))
+
+
+def moe_gate_backward(T, H, E, d_logits_bf16, x, gate_w, dx_in, dx, d_gate, grad_dtype=MOE_BF16, accumulate=False,
+                      dev_status=None, stream=None):
+    """dx = dx_in + d_logits gate and d_gate = d_logits^T x; either may be None."""
+    bf, gt = torch.bfloat16, _grad("moe_gate_backward", grad_dtype)
+    _expect("moe_gate_backward", d_logits_bf16=(d_logits_bf16, T * E, bf), x=(x, T * H, bf), gate_w=(gate_w, E * H, bf),
+            dx_in=(dx_in, T * H, bf), dx=(dx, T * H, bf), d_gate=(d_gate, E * H, gt))
+    _check("moe_gate_backward", load_library().moe_gate_backward(
+        T, H, E, _ptr(d_logits_bf16), _ptr(x), _ptr(gate_w), _ptr(dx_in), _ptr(dx), _ptr(d_gate), grad_dtype,
+        int(bool(accumulate)), _ptr(dev_status), _stream(stream)))
 
 
 def moe_combine(T, k, H, expert_out, slot_to_row, topk_w, shared_out, y, stream=None):
