@@ -719,6 +719,22 @@ moe_status make_out_tmap(CUtensorMap* m, const void* ptr, bool f32, uint64_t inn
   return MOE_OK;
 }
 
+// A row-major bf16 matrix [rows, cols] as [cols / 64] blocks of [rows, 64];
+// boxes of 64 rows of two blocks.
+moe_status make_block_tmap(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
+  cuuint64_t dims[3] = {64, rows, cols / 64};
+  cuuint64_t strides[2] = {cols * 2, 128};
+  cuuint32_t box[3] = {64, 64, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
+  return MOE_OK;
+}
+
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // Parts of moe_swiglu_ffn_backward's workspace.
@@ -737,19 +753,19 @@ BackwardWs backward_ws(int32_t rows, int32_t I) {
 
 // One weight-gradient product: C[g] [M, N] from A [rows, M] and B [rows, N].
 moe_status plan_wgrad(WgradProblem* p, int32_t rows, int32_t groups, const void* A, int32_t M, const void* B, int32_t N,
-                      void* out, bool f32, int subs) {
-  moe_status s = make_tmap(&p->tmA, A, false, M, rows, 64);
+                      void* out, bool f32) {
+  p->a_flat = M % 64 != 0;
+  moe_status s = p->a_flat ? make_tmap(&p->tmA, A, false, M, rows, 64) : make_block_tmap(&p->tmA, A, M, rows);
   if (s != MOE_OK) return s;
-  if ((s = make_tmap(&p->tmB, B, false, N, rows, 64)) != MOE_OK) return s;
+  if ((s = make_block_tmap(&p->tmB, B, N, rows)) != MOE_OK) return s;
   if ((s = make_out_tmap(&p->tmOut, out, f32, N, static_cast<uint64_t>(groups) * M, 32)) != MOE_OK) return s;
   p->M = M;
   p->N = N;
-  p->tiles = groups * ((M + 128 * subs - 1) / (128 * subs)) * ((N + 255) / 256);
+  p->n_blocks = (N + 255) / 256;
+  p->per_group = (M + 255) / 256 * p->n_blocks;
+  p->tiles = groups * p->per_group;
   return MOE_OK;
 }
-
-// Features per wgrad tile (in units of 128): see wgrad_kernel.
-int wgrad_subs(int32_t rows, int32_t groups) { return rows / groups >= 512 ? 2 : 1; }
 
 bool grad_args_ok(moe_dtype grad_dtype, int32_t accumulate) {
   if (grad_dtype != MOE_BF16 && grad_dtype != MOE_F32) return false;
@@ -830,15 +846,14 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
     if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
   }
   if (d_w13 || d_w2) {
-    const int subs = wgrad_subs(rows, w->groups);
     WgradArgs q{};
     const bool f32 = grad_dtype == MOE_F32;
     if (d_w13) {
-      s = plan_wgrad(&q.prob[q.n_prob++], rows, w->groups, d_gu, 2 * I, a, H, d_w13, f32, subs);
+      s = plan_wgrad(&q.prob[q.n_prob++], rows, w->groups, d_gu, 2 * I, a, H, d_w13, f32);
       if (s != MOE_OK) return s;
     }
     if (d_w2) {
-      s = plan_wgrad(&q.prob[q.n_prob++], rows, w->groups, d_out, H, hw, I, d_w2, f32, subs);
+      s = plan_wgrad(&q.prob[q.n_prob++], rows, w->groups, d_out, H, hw, I, d_w2, f32);
       if (s != MOE_OK) return s;
     }
     q.rows = rows;
@@ -848,7 +863,7 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
     q.accumulate = accumulate;
     q.status = dev_status;
     q.wait_ns = wait_limit();
-    s = check_launch(launch_wgrad(subs, q, nsm, st));
+    s = check_launch(launch_wgrad(q, nsm, st));
   }
   return s;
 }
@@ -897,7 +912,7 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
   }
   if (d_gate) {                                        // d_gate = d_logits^T x
     WgradArgs q{};
-    if ((s = plan_wgrad(&q.prob[0], T, 1, d_logits_bf16, E, x, H, d_gate, grad_dtype == MOE_F32, 1)) != MOE_OK) return s;
+    if ((s = plan_wgrad(&q.prob[0], T, 1, d_logits_bf16, E, x, H, d_gate, grad_dtype == MOE_F32)) != MOE_OK) return s;
     q.n_prob = 1;
     q.rows = T;
     q.groups = 1;
@@ -905,7 +920,7 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
     q.accumulate = accumulate;
     q.status = dev_status;
     q.wait_ns = wait_limit();
-    s = check_launch(launch_wgrad(1, q, nsm, st));
+    s = check_launch(launch_wgrad(q, nsm, st));
   }
   return s;
 }

@@ -42,7 +42,9 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
 }
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
-__device__ __forceinline__ float sigmoid_fast(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+// The full-precision exponential: d_row_w is an fp32 output, and __expf's
+// error would be the largest in it.
+__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
 
 // ========================================================================
 // Products of a segment's rows with a weight
@@ -290,7 +292,7 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float wj = __shfl_sync(0xffffffffu, w, j);
-            const float sg = sigmoid_fast(g[j]);
+            const float sg = sigmoid(g[j]);
             const float act = g[j] * sg;                            // SiLU(g)
             const float dh = v[j] * wj;
             const float h = act * u[j];
@@ -343,74 +345,167 @@ row_w_grad_kernel(int rows, int n, const float* __restrict__ partial, const int3
 // ========================================================================
 // Weight gradients: C[g] [M, N] = A[rows of g, M]^T B[rows of g, N]
 // ========================================================================
-// Tile: 128 x SUBS features of A by 256 features of B (128 where N leaves no
-// more), K = the segment's rows in blocks of 64. SUBS = 1: two accumulators of
-// 256 TMEM columns, so a tile's epilogue overlaps the next tile's products,
-// which is what counts where a segment has few rows and the output's bytes
-// bound the work; SUBS = 2: one accumulator pair, half the operand bytes per
-// product, for segments long enough that the products bound it.
-// Warp 0 loads (four or two boxes of 64 rows x 64 features per operand), warp 1
-// zeroes rows behind the segment's end in its last block and issues the MMAs,
-// the other eight take the accumulator to shared memory as 128-byte-swizzled
+// A pair of CTAs (a cluster of two) shares one tile of 256 features of A by 256
+// of B (128 where N leaves no more), K = the segment's rows in blocks of 64:
+// tcgen05.mma.cta_group::2 with M = 256. Each CTA holds 128 features of A and
+// half of B's in shared memory and the accumulator rows of its 128 features in
+// TMEM. A CTA so loads 32 KB per block for the products a lone CTA would load
+// 48 KB for, and the accumulator takes 256 of the 512 TMEM columns: two of them,
+// so a tile's epilogue overlaps the next tile's products. Both count: where a
+// segment has few rows the output's bytes bound the work, else the operands'
+// way from L2 does. Measured on B200 (V3 widths, 32 experts): one CTA per tile
+// of 128 x 256 with two accumulators 933 us at 256 rows per expert and 2815 us
+// at 1024; 256 x 256 with one accumulator 935 and 2523 us.
+//
+// Warp 0 loads its CTA's operands (64 rows x 128 features a load); both CTAs'
+// loads complete on the first CTA's full_bar, whose warp 1 issues the MMAs for
+// both and commits to both. A last block with rows behind the segment's end in
+// its last step goes another way: each CTA's loads complete on a barrier of its
+// own, its last warp zeroes those rows and arrives on the first CTA's
+// tail_done. (With such a handshake for every block, or the zeroing on the MMA
+// warp, its latency set the pace: 251 rows per expert cost 1.5 times what 256
+// do.) Eight warps take the accumulator to shared memory as 128-byte-swizzled
 // boxes and store them with TMA (bf16, or fp32 added to what is there).
-template <int SUBS>
 struct WgradCfg {
-  static constexpr int STAGES = SUBS == 2 ? 3 : 4;
-  static constexpr uint32_t A_BYTES = SUBS * 2 * kChunkBytes;
-  static constexpr uint32_t STAGE_BYTES = A_BYTES + 4 * kChunkBytes;
-  static constexpr int ACCS = SUBS == 2 ? 1 : 2;
+  static constexpr int KB = 64;                          // rows per stage
+  static constexpr int STAGES = 6;
+  static constexpr uint32_t PAIR = 2 * kChunkBytes;      // one load: KB rows x 128 features, as two 64-feature boxes
+  static constexpr uint32_t STAGE_BYTES = 2 * PAIR;      // A's, then B's
   static constexpr int EPIW = 8;
-  static constexpr uint32_t OUT_BYTES = EPIW * 32 * 128;
-  static constexpr size_t SMEM = STAGES * STAGE_BYTES + OUT_BYTES + 1024;
+  static constexpr int THREADS = 96 + 32 * EPIW;         // loads, MMAs, epilogue, tails
 };
+// All shared memory of the kernel: the stages take all but a few KB of the
+// SM's, so nothing is left for a static allocation beside an aligned dynamic one.
+struct WgradSmem {
+  using C = WgradCfg;
+  uint8_t stage[C::STAGES][C::STAGE_BYTES];              // 1024-byte aligned
+  uint8_t out[C::EPIW][32 * 128];
+  uint64_t full_bar[C::STAGES], tail_full[C::STAGES], tail_done[C::STAGES], empty_bar[C::STAGES];
+  uint64_t tmem_full[2], tmem_empty[2], drain_bar;
+  uint32_t tmem_base;
+  uint32_t loads[C::STAGES], tails[C::STAGES];           // loads issued into a stage, on full_bar and on tail_full
+  int abort_flag;
+  int off[kMaxGroups + 1];
+};
+
+// Loads of a CTA of a pair into its own shared memory, completing on a barrier
+// of either CTA (`bar`: its address in the cluster). 3-D: one box of a matrix
+// seen as [N / 64] column blocks of [rows, 64]: 64 rows of two column blocks,
+// each block's rows contiguous in shared memory.
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t row,
+                                                 int32_t block, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row), "r"(block), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                                 int32_t y, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+// A 32-bit shared variable of the other CTA.
+__device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
+// The CTA-pair forms of the tcgen05 calls.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once every MMA issued so far by this thread is done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// Arrives on the first CTA's copy of `bar` (release at cluster scope); relaxed
+// where the thread has written nothing that is read after the barrier.
+__device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_first_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
+               : "memory");
+}
 
 struct WgradTile { int p, g, m, n, k0, kn; };
 
-__device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, int t, int subs) {
+// `off`: the segments' starts in shared memory, cut to the rows there are.
+__device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* off, int t) {
   WgradTile w;
   w.p = a.n_prob > 1 && t >= a.prob[0].tiles ? 1 : 0;
   if (w.p) t -= a.prob[0].tiles;
   const WgradProblem& pr = a.prob[w.p];
-  const int per = pr.tiles / a.groups;
-  w.g = t / per;
-  const int r = t - w.g * per;
-  const int nn = (pr.N + 255) / 256;
-  w.m = (r / nn) * 128 * subs;
-  w.n = (r - (r / nn) * nn) * 256;
-  w.k0 = a.offsets ? min(max(__ldg(a.offsets + w.g), 0), a.rows) : 0;      // cut to the rows there are
-  w.kn = a.offsets ? min(__ldg(a.offsets + w.g + 1), a.rows) - w.k0 : a.rows;
+  w.g = t / pr.per_group;
+  const int r = t - w.g * pr.per_group;
+  const int mi = r / pr.n_blocks;
+  w.m = mi * 256;
+  w.n = (r - mi * pr.n_blocks) * 256;
+  w.k0 = off[w.g];
+  w.kn = off[w.g + 1] - w.k0;
   return w;
 }
 
-template <int SUBS>
-__global__ void __launch_bounds__(64 + 32 * WgradCfg<SUBS>::EPIW, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WgradCfg::THREADS, 1)
 wgrad_kernel(const __grid_constant__ WgradArgs a) {
-  using C = WgradCfg<SUBS>;
-  constexpr int KB = 64, STAGES = C::STAGES, ACCS = C::ACCS, EPIW = C::EPIW;
+  using C = WgradCfg;
+  constexpr int KB = C::KB, STAGES = C::STAGES, EPIW = C::EPIW;
   extern __shared__ __align__(1024) uint8_t dsmem[];
-  __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
-  __shared__ uint64_t tmem_full[ACCS], tmem_empty[ACCS], drain_bar;
-  __shared__ uint32_t tmem_base_s;
-  __shared__ int issued_parity[STAGES];
-  __shared__ volatile int abort_flag;
+  WgradSmem& sm = *reinterpret_cast<WgradSmem*>(dsmem);
+  if ((smem_u32(dsmem) & 1023u) != 0) {                            // the swizzled tiles need it (the same in both CTAs)
+    flag_status(a.status, MOE_DEVSTAT_TIMEOUT);
+    return;
+  }
+  uint64_t *full_bar = sm.full_bar, *empty_bar = sm.empty_bar, *tmem_full = sm.tmem_full, *tmem_empty = sm.tmem_empty;
+  const int* off = sm.off;
+  volatile int* abort_flag = &sm.abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
-  auto sA = [&](int st) { return smem + st * C::STAGE_BYTES; };
-  auto sB = [&](int st) { return smem + st * C::STAGE_BYTES + C::A_BYTES; };
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int first = static_cast<int>(cluster_id_x()), stride = static_cast<int>(gridDim.x) / 2;
+  for (int i = threadIdx.x; i <= a.groups; i += blockDim.x)
+    sm.off[i] = a.offsets ? min(max(a.offsets[i], 0), a.rows) : i * a.rows;
+  auto sA = [&](int st) { return sm.stage[st]; };
+  auto sB = [&](int st) { return sm.stage[st] + C::PAIR; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full_bar[i], 1);
+      mbar_init(&sm.tail_full[i], 1);
+      mbar_init(&sm.tail_done[i], 2);                            // both CTAs' tail warps
       mbar_init(&empty_bar[i], 1);
-      issued_parity[i] = -1;
+      sm.loads[i] = sm.tails[i] = 0;
     }
-    for (int i = 0; i < ACCS; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&tmem_full[i], 1);
-      mbar_init(&tmem_empty[i], 32 * EPIW);
+      mbar_init(&tmem_empty[i], 2 * EPIW);                         // one arrival per epilogue warp of both CTAs
     }
-    mbar_init(&drain_bar, 1);
-    abort_flag = 0;
+    mbar_init(&sm.drain_bar, 1);
+    sm.abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -420,14 +515,12 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       tma_prefetch_desc(&a.prob[p].tmOut);
     }
   }
-  if (warp == 1) {
-    tmem_alloc(&tmem_base_s, 512);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 512);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                                                  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
-  const uint32_t tmem_base = tmem_base_s;
+  const uint32_t tmem_base = sm.tmem_base;
   const int total = a.prob[0].tiles + (a.n_prob > 1 ? a.prob[1].tiles : 0);
 
   if (warp == 0) {
@@ -436,158 +529,213 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < total && ok && !abort_flag; t += gridDim.x) {
-        const WgradTile w = wgrad_tile(a, t, SUBS);
+      for (int t = first; t < total && ok && !*abort_flag; t += stride) {
+        const WgradTile w = wgrad_tile(a, off, t);
         const WgradProblem& pr = a.prob[w.p];
-        const int nbx = pr.N - w.n > 128 ? 4 : 2;                  // boxes of B
-        const uint32_t bytes = C::A_BYTES + static_cast<uint32_t>(nbx) * kChunkBytes;
+        const int m = w.m + 128 * rank;
+        const int nb = w.n / 64 + (pr.N - w.n > 128 ? 2 : 1) * rank;    // this CTA's half of B's features
         for (int k = 0; k < w.kn; k += KB) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag, a.status, a.wait_ns)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full_bar[stage], bytes);
-#pragma unroll
-          for (int j = 0; j < 2 * SUBS; ++j)
-            tma_load_2d(sA(stage) + j * kChunkBytes, &pr.tmA, &full_bar[stage], w.m + 64 * j, w.k0 + k, pol);
-          for (int j = 0; j < nbx; ++j)
-            tma_load_2d(sB(stage) + j * kChunkBytes, &pr.tmB, &full_bar[stage], w.n + 64 * j, w.k0 + k, pol);
-          issued_parity[stage] = static_cast<int>(phase);
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, a.status, a.wait_ns)) { ok = false; break; }
+          const bool tail = w.kn - k <= KB && (w.kn & 15);         // rows to zero
+          uint32_t bar;
+          if (tail) {
+            mbar_arrive_expect_tx(&sm.tail_full[stage], C::STAGE_BYTES);
+            bar = mapa_shared(smem_u32(&sm.tail_full[stage]), rank);
+            ++sm.tails[stage];
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::STAGE_BYTES);
+            bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+            ++sm.loads[stage];
+          }
+          if (pr.a_flat) {                                         // rows not a whole number of boxes wide
+            tma_load_2d_pair(sA(stage), &pr.tmA, bar, m, w.k0 + k, pol);
+            tma_load_2d_pair(sA(stage) + kChunkBytes, &pr.tmA, bar, m + 64, w.k0 + k, pol);
+          } else {
+            tma_load_3d_pair(sA(stage), &pr.tmA, bar, w.k0 + k, m / 64, pol);
+          }
+          tma_load_3d_pair(sB(stage), &pr.tmB, bar, w.k0 + k, nb, pol);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (abort_flag) {
+      if (*abort_flag)                                             // this CTA's tail loads; the others: below
         for (int i = 0; i < STAGES; ++i)
-          if (issued_parity[i] >= 0) mbar_wait_drain(&full_bar[i], static_cast<uint32_t>(issued_parity[i]));
-      }
+          if (sm.tails[i]) mbar_wait_drain(&sm.tail_full[i], (sm.tails[i] - 1) & 1u);
     }
   } else if (warp == 1) {
-    int stage = 0;
-    uint32_t phase = 0, it = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
-      const WgradTile w = wgrad_tile(a, t, SUBS);
-      const WgradProblem& pr = a.prob[w.p];
-      const int nbx = pr.N - w.n > 128 ? 4 : 2;
-      const uint32_t idesc = make_idesc(1u, 128u, nbx == 4 ? 256u : 128u) | kIdescAMn | kIdescBMn;
-      const uint32_t acc_i = ACCS == 2 ? (it & 1u) : 0u;
-      const uint32_t acc_ph = ACCS == 2 ? ((it >> 1) & 1u) : (it & 1u);
-      const uint32_t d0 = tmem_base + acc_i * 256;
-      if (lane == 0) ok = mbar_wait(&tmem_empty[acc_i], acc_ph ^ 1u, &abort_flag, a.status, a.wait_ns);
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (!ok) break;
-      tc_fence_after();
-      for (int k = 0; k < w.kn; k += KB) {
-        if (lane == 0) ok = mbar_wait(&full_bar[stage], phase, &abort_flag, a.status, a.wait_ns);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    if (rank == 0 && lane == 0) {
+      // Nothing but the wait stands between one block's MMAs and the next's:
+      // their issue keeps only a few queued, and 700 cycles of bookkeeping a
+      // block (512 of MMAs) cost a third of the rate.
+      const uint64_t ad0 = mn_desc(smem_u32(sm.stage[0]));         // descriptor of stage 0's A
+      int st = 0;
+      uint32_t it = 0, full_par = 0, tail_par = 0;                 // parity of each stage's next wait, by barrier
+      bool ok = true;
+      for (int t = first; t < total && ok; t += stride, ++it) {
+        const WgradTile w = wgrad_tile(a, off, t);
+        const uint32_t idesc = make_idesc(1u, 256u, a.prob[w.p].N - w.n > 128 ? 256u : 128u) | kIdescAMn | kIdescBMn;
+        const uint32_t d0 = tmem_base + (it & 1u) * 256;
+        const int even = w.kn / KB, rest = w.kn - even * KB;       // blocks of 64 rows, and the last one's rows
+        ok = mbar_wait(&tmem_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, abort_flag, a.status, a.wait_ns);
         if (!ok) break;
-        const int valid = min(KB, w.kn - k);                       // rows of this block in the segment
-        const int steps = (valid + 15) / 16;
-        if (valid & 15) {                                          // zero the last step's rows behind the end
-          const int nz = (steps * 16 - valid) * 8;                 // 16-byte pieces per box
-          const int boxes = 2 * SUBS + nbx;                        // A's boxes, then B's, are adjacent
-          uint8_t* base = sA(stage) + valid * 128;
-          for (int i = lane; i < nz * boxes; i += 32) {
-            const int b = i / nz;
-            *reinterpret_cast<uint4*>(base + b * kChunkBytes + (i - b * nz) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async();
-          __syncwarp();
-        }
-        if (lane == 0) {
+        tc_fence_after();
+        uint32_t acc = 0;
+        for (int kb = 0; kb < even; ++kb) {
+          ok = mbar_wait(&full_bar[st], (full_par >> st) & 1u, abort_flag, a.status, a.wait_ns);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA(stage)), b0 = smem_u32(sB(stage));
-          for (int kk = 0; kk < steps; ++kk) {
-            const uint32_t acc = (k | kk) != 0;
-            const uint64_t bd = mn_desc(b0 + kk * 2048);
-            umma_bf16(d0, mn_desc(a0 + kk * 2048), bd, idesc, acc);
-            if (SUBS == 2) umma_bf16(d0 + 256, mn_desc(a0 + 2 * kChunkBytes + kk * 2048), bd, idesc, acc);
+          const uint64_t ad = ad0 + st * (C::STAGE_BYTES >> 4), bd = ad + (C::PAIR >> 4);
+#pragma unroll
+          for (int kk = 0; kk < KB / 16; ++kk) {                   // 2048 B a step, in the descriptors' 16-byte units
+            umma_bf16_pair(d0, ad + kk * 128, bd + kk * 128, idesc, acc);
+            acc = 1;
           }
-          umma_commit(&empty_bar[stage]);
+          umma_commit_pair(&empty_bar[st]);
+          full_par ^= 1u << st;
+          if (++st == STAGES) st = 0;
         }
-        __syncwarp();
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (ok && rest > 0) {
+          if (rest & 15) {
+            ok = mbar_wait(&sm.tail_done[st], (tail_par >> st) & 1u, abort_flag, a.status, a.wait_ns);
+            tail_par ^= 1u << st;
+          } else {
+            ok = mbar_wait(&full_bar[st], (full_par >> st) & 1u, abort_flag, a.status, a.wait_ns);
+            full_par ^= 1u << st;
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ad = ad0 + st * (C::STAGE_BYTES >> 4), bd = ad + (C::PAIR >> 4);
+          for (int kk = 0; kk < (rest + 15) / 16; ++kk) {
+            umma_bf16_pair(d0, ad + kk * 128, bd + kk * 128, idesc, acc);
+            acc = 1;
+          }
+          umma_commit_pair(&empty_bar[st]);
+          if (++st == STAGES) st = 0;
+        }
+        if (ok) umma_commit_pair(&tmem_full[it & 1u]);
       }
-      if (!ok) break;
-      if (lane == 0) umma_commit(&tmem_full[acc_i]);
+      // all issued MMAs must finish before TMEM is released
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                       smem_u32(&sm.drain_bar))
+                   : "memory");
+      mbar_wait_drain(&sm.drain_bar, 0);
     }
-    if (lane == 0) {
-      umma_commit(&drain_bar);
-      mbar_wait_drain(&drain_bar, 0);
+  } else if (warp == 2 + EPIW) {
+    // rows behind the segment's end in the last block: zeroed as soon as they land
+    int stage = 0;
+    uint32_t par = 0;
+    for (int t = first; t < total; t += stride) {
+      const WgradTile w = wgrad_tile(a, off, t);
+      const int blocks = (max(w.kn, 0) + KB - 1) / KB;
+      if (w.kn & 15) {
+        const int st = (stage + blocks - 1) % STAGES;
+        const int valid = w.kn - (blocks - 1) * KB;
+        bool ok = true;
+        if (lane == 0) ok = mbar_wait(&sm.tail_full[st], (par >> st) & 1u, abort_flag, a.status, a.wait_ns);
+        if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0) == 0) break;
+        par ^= 1u << st;
+        const int nz = ((valid + 15) / 16 * 16 - valid) * 128;     // bytes per box: A's two boxes, then B's
+        uint8_t* base = sA(st) + valid * 128;
+        for (int i = lane * 16; i < nz; i += 512)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) *reinterpret_cast<uint4*>(base + b * kChunkBytes + i) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_first(&sm.tail_done[st]);
+      }
+      stage = (stage + blocks) % STAGES;
     }
   } else {
     const int q = warp & 3, half = (warp - 2) / 4;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-    uint8_t* box = smem + STAGES * C::STAGE_BYTES + (warp - 2) * 32 * 128;
+    uint8_t* box = sm.out[warp - 2];
     const int cols = a.f32 ? 32 : 64;                              // columns of a 128-byte box row
     uint32_t it = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
-      const WgradTile w = wgrad_tile(a, t, SUBS);
+    for (int t = first; t < total; t += stride, ++it) {
+      const WgradTile w = wgrad_tile(a, off, t);
       const WgradProblem& pr = a.prob[w.p];
       const int width = pr.N - w.n > 128 ? 256 : 128;
-      const uint32_t acc_i = ACCS == 2 ? (it & 1u) : 0u;
-      const uint32_t acc_ph = ACCS == 2 ? ((it >> 1) & 1u) : (it & 1u);
-      if (!mbar_wait(&tmem_full[acc_i], acc_ph, &abort_flag, a.status, a.wait_ns)) break;
+      const int m = w.m + 128 * rank + 32 * q;                     // this warp's 32 features of A
+      const uint32_t acc = lane_addr + (it & 1u) * 256;
+      if (!mbar_wait(&tmem_full[it & 1u], (it >> 1) & 1u, abort_flag, a.status, a.wait_ns)) break;
       tc_fence_after();
       const bool empty = w.kn <= 0;
-      if (!(empty && a.accumulate)) {                              // adding nothing needs no store
-#pragma unroll 1
-        for (int s = 0; s < SUBS; ++s) {
-          const int y = w.g * pr.M + w.m + s * 128 + 32 * q;
-          if (w.m + s * 128 + 32 * q >= pr.M) continue;            // rows past the matrix: nothing to store
-          for (int c = half * cols; c < width; c += 2 * cols) {
-            float v[32], v2[32];
-            if (!empty) {
-              tmem_ld32(lane_addr + acc_i * 256 + s * 256 + c, v);
-              if (!a.f32) tmem_ld32(lane_addr + acc_i * 256 + s * 256 + c + 32, v2);
-              tmem_ld_wait();
-            } else {
+      // adding nothing needs no store, and rows past the matrix have none
+      if (!(empty && a.accumulate) && m < pr.M) {
+        for (int c = half * cols; c < width; c += 2 * cols) {
+          float v[32], v2[32];
+          if (!empty) {
+            tmem_ld32(acc + c, v);
+            if (!a.f32) tmem_ld32(acc + c + 32, v2);
+            tmem_ld_wait();
+          } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = v2[j] = 0.0f;
+            for (int j = 0; j < 32; ++j) v[j] = v2[j] = 0.0f;
+          }
+          // the last store of this box has been read
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+          uint8_t* row = box + lane * 128;
+          if (a.f32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float* f = i < 4 ? v + 8 * i : v2 + 8 * (i - 4);
+              uint4 u;
+              __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+              *reinterpret_cast<uint4*>(row + ((i ^ (lane & 7)) << 4)) = u;
             }
-            // the previous store of this box has been read
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
-            uint8_t* row = box + lane * 128;
-            if (a.f32) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) =
-                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float* f = i < 4 ? v + 8 * i : v2 + 8 * (i - 4);
-                uint4 u;
-                __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-                *reinterpret_cast<uint4*>(row + ((i ^ (lane & 7)) << 4)) = u;
-              }
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              if (a.accumulate)
-                asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];"
-                             ::"l"(reinterpret_cast<uint64_t>(&pr.tmOut)), "r"(smem_u32(box)), "r"(w.n + c), "r"(y)
-                             : "memory");
-              else
-                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
-                             ::"l"(reinterpret_cast<uint64_t>(&pr.tmOut)), "r"(smem_u32(box)), "r"(w.n + c), "r"(y)
-                             : "memory");
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            const int y = w.g * pr.M + m;
+            if (a.accumulate)
+              asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];"
+                           ::"l"(reinterpret_cast<uint64_t>(&pr.tmOut)), "r"(smem_u32(box)), "r"(w.n + c), "r"(y)
+                           : "memory");
+            else
+              asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+                           ::"l"(reinterpret_cast<uint64_t>(&pr.tmOut)), "r"(smem_u32(box)), "r"(w.n + c), "r"(y)
+                           : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         }
       }
       tc_fence_before();
-      mbar_arrive(&tmem_empty[acc_i]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[it & 1u]);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                                                  // neither CTA issues anything any more
+  // After an abort one CTA may have loaded into a stage what the other had not
+  // got to: complete the phases both started, arm the one only the second
+  // started, so that every load has landed before either CTA leaves.
+  if (rank == 0 && threadIdx.x == 0 && (*abort_flag || ld_cluster(&sm.abort_flag, 1) != 0)) {
+    for (int i = 0; i < STAGES; ++i) {
+      const uint32_t mine = sm.loads[i], theirs = ld_cluster(&sm.loads[i], 1);
+      if (mine > theirs)
+        asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full_bar[i])),
+                     "r"(C::STAGE_BYTES)
+                     : "memory");
+      else if (theirs > mine)
+        mbar_arrive_expect_tx(&full_bar[i], C::STAGE_BYTES);
+      const uint32_t n = mine > theirs ? mine : theirs;
+      if (n) mbar_wait_drain(&full_bar[i], (n - 1) & 1u);
+    }
+  }
+  cluster_sync();                                                  // nothing of either CTA is used any more
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, 512);
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
 }
 
 // ========================================================================
@@ -709,17 +857,15 @@ cudaError_t launch_route_backward(int T, int E, int k, int scoring, int norm, fl
   return cudaGetLastError();
 }
 
-template <int SUBS>
-static cudaError_t wgrad(const WgradArgs& a, int grid, cudaStream_t stream) {
-  using C = WgradCfg<SUBS>;
-  cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<SUBS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(C::SMEM));
+cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(WgradSmem);
+  static_assert(smem <= 232448, "wgrad_kernel's shared memory exceeds an SM's");
+  cudaError_t e = cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  wgrad_kernel<SUBS><<<grid, 64 + 32 * C::EPIW, C::SMEM, stream>>>(a);
+  const int tiles = a.prob[0].tiles + (a.n_prob > 1 ? a.prob[1].tiles : 0);
+  const int pairs = num_sms / 2 < tiles ? num_sms / 2 : tiles;
+  wgrad_kernel<<<2 * pairs, WgradCfg::THREADS, smem, stream>>>(a);
   return cudaGetLastError();
-}
-cudaError_t launch_wgrad(int subs, const WgradArgs& a, int grid, cudaStream_t stream) {
-  return subs == 2 ? wgrad<2>(a, grid, stream) : wgrad<1>(a, grid, stream);
 }
 
 }  // namespace moe

@@ -34,9 +34,11 @@ cudaError_t launch_row_w_grad(int rows, int n, const float* partial, const int32
 // Weight gradients C[g] [M, N] = A[rows of g]^T B[rows of g]; up to two such
 // products over the same segments in one launch.
 struct WgradProblem {
-  CUtensorMap tmA, tmB;               // [rows, M], [rows, N] bf16, boxes of 64 rows x 64 columns
+  CUtensorMap tmA, tmB;               // [rows, M], [rows, N] bf16 as column blocks: 64 rows x 2 blocks of 64
   CUtensorMap tmOut;                  // [groups * M, N], boxes of 32 rows x 128 bytes
-  int32_t M, N, tiles;
+  int32_t M, N, tiles;                // tiles = groups * per_group
+  int32_t a_flat;                     // M % 64 != 0: tmA is the plain matrix, boxes of 64 rows x 64 columns
+  int32_t per_group, n_blocks;        // tiles of a group; its blocks along N
 };
 struct WgradArgs {
   WgradProblem prob[2];
@@ -46,7 +48,7 @@ struct WgradArgs {
   int32_t* status;
   uint64_t wait_ns;
 };
-cudaError_t launch_wgrad(int subs, const WgradArgs& a, int grid, cudaStream_t stream);
+cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_route_backward(int T, int E, int k, int scoring, int norm, float scale, const float* logits,
                                   const int32_t* ids, const float* d_w, const int32_t* slot_to_row, float* d_logits,
                                   void* d_logits16, int32_t* status, cudaStream_t stream);
