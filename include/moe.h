@@ -71,6 +71,7 @@ typedef int32_t moe_dtype;
 #define MOE_F32  0
 #define MOE_BF16 1
 #define MOE_E4M3 2   /* float8 e4m3 "fn": bias 7, max 448, no inf */
+#define MOE_MXFP4 3  /* e2m1 values, two a byte, one e8m0 scale per 32 */
 
 typedef int32_t moe_scoring;
 #define MOE_SOFTMAX 0
@@ -243,15 +244,21 @@ MOE_API moe_status moe_permute_static_ws(int32_t T, int32_t k, int32_t E, int32_
  *             values in the tiled layout moe_tile_ffn_weights writes.
  *             MOE_E4M3 weights carry fp32 block scales
  *             w13_scale [groups, 2I/128, H/128], w2_scale [groups, H/128,
- *             I/128] (moe_quantize_blocks).
+ *             I/128] (moe_quantize_blocks). MOE_MXFP4 weights are packed codes
+ *             [groups, 2I, H/2], [groups, H, I/2] with the scales
+ *             moe_quantize_mxfp4_weights lays out (pass them as w13_scale /
+ *             w2_scale).
  *   a         [rows, H] activations: bf16, or e4m3 codes with a_scale
- *             [rows, H/128] when w->dtype == MOE_E4M3.
+ *             [rows, H/128] when w->dtype == MOE_E4M3; MOE_MXFP4: codes
+ *             [rows, H/2] and scales from moe_quantize_mxfp4_rows.
  *   offsets   [groups+1] device int32 segment starts (from moe_permute), or
  *             NULL: one group covering all rows (groups must be 1).
  *   row_w     [rows] fp32 per-row output weight fused into the epilogue of
  *             the second GEMM, or NULL (= 1).
  *   h_ws      [rows, I] intermediate: bf16, or e4m3 codes with h_scale_ws
- *             [rows, I/128] for MOE_E4M3 (re-quantised per 1x128 tile).
+ *             [rows, I/128] for MOE_E4M3 (re-quantised per 1x128 tile), or
+ *             codes [rows, I/2] with scales [I/128, rows] words for MOE_MXFP4
+ *             (h quantised from its fp32 values).
  *   out       [rows, H] bf16 = row_w * (SiLU(a w1^T) * (a w3^T)) w2^T.
  * Limits: I % 128 == 0, H % 256 == 0, rows >= 1. E4M3 also needs H % 128
  * and I % 128. Accumulation is fp32 on the tensor cores; h is rounded to
@@ -260,9 +267,9 @@ MOE_API moe_status moe_permute_static_ws(int32_t T, int32_t k, int32_t E, int32_
 typedef struct {
     const void* w13;
     const void* w2;
-    const float* w13_scale;   /* E4M3 only, else NULL */
-    const float* w2_scale;    /* E4M3 only, else NULL */
-    moe_dtype dtype;          /* MOE_BF16 or MOE_E4M3 */
+    const float* w13_scale;   /* E4M3; MXFP4: scale bytes; else NULL */
+    const float* w2_scale;    /* E4M3; MXFP4: scale bytes; else NULL */
+    moe_dtype dtype;          /* MOE_BF16, MOE_E4M3 or MOE_MXFP4 */
     int32_t groups;
     int32_t I;
     int32_t tiled;            /* bf16 only: 1 = w13 / w2 in the tiled layout, 0 = row-major */
@@ -300,8 +307,8 @@ MOE_API moe_status moe_down_proj(int32_t rows, int32_t H, const moe_ffn_weights*
  * dtype; its I may differ from w's). rows / sh_rows: T*k / T. Other
  * arguments, limits and errors as moe_gate_up_swiglu / moe_down_proj; E4M3
  * scales as there (sh_a_scale / sh_h_scale for the shared rows). bf16 layers
- * run as one launch; E4M3 layers as two launches of the same calls in this
- * order. */
+ * run as one launch; E4M3 and MXFP4 layers as two launches of the same calls in
+ * this order. */
 MOE_API moe_status moe_gate_up_swiglu_with_shared(int32_t rows, int32_t H, const moe_ffn_weights* w,
                               const void* a, const float* a_scale, const int32_t* offsets,
                               void* h_ws, float* h_scale_ws,
@@ -534,6 +541,32 @@ MOE_API moe_status moe_quantize_blocks(int32_t batch, int32_t N, int32_t K, cons
                                void* q, float* scale, void* stream);
 MOE_API moe_status moe_quantize_rows(int32_t M, int32_t K, const void* a, void* q,
                              float* scale, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * Microscaled 4-bit floating point (MXFP4): E2M1 values (0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives; value 2i in the low half of byte i, 2i + 1 in the
+ * high one) with one E8M0 scale byte s, 2^(s - 127), per 32 consecutive values
+ * of K. The layer's pages stop at FP8; the format is the OCP microscaling one.
+ *   scale: s - 127 = floor(log2 amax) - 2 within [-127, 125]; s = 127 for a
+ *          block of zeros; s = 255 (NaN) for a block with NaN or infinity.
+ *   code:  nearest of v / 2^(s - 127), ties to the even code, above 6 to 6.
+ * moe_quantize_mxfp4_rows: row r of the result is row src_rows[r] of a
+ *   [a_rows, K] bf16 (NULL: row r; then a_rows >= rows), so that a layer's
+ *   permutation (src_token of moe_permute) happens on the way. q [rows, K/2]
+ *   codes; scale [K/128, rows] 32-bit words, byte i of word (kk, r) the scale of
+ *   row r's values [128 kk + 32 i, +32). A source row outside [0, a_rows) gives
+ *   a row of zeros and flags MOE_DEVSTAT_BAD_EXPERT_ID. K % 128 == 0.
+ * moe_dequantize_mxfp4_rows: out [rows, K] bf16, the values (exact).
+ * moe_quantize_mxfp4_weights: w [batch, N, K] bf16 -> q [batch, N, K/2] and
+ *   scale [batch, N/128, K/128, 512]: row r's word of a 128 x 128 block at byte
+ *   (r % 32) * 16 + (r / 32) * 4. N % 128 == 0, K % 128 == 0.
+ * ------------------------------------------------------------------------ */
+MOE_API moe_status moe_quantize_mxfp4_rows(int32_t rows, int32_t K, const void* a, int32_t a_rows,
+                              const int32_t* src_rows, void* q, void* scale, int32_t* dev_status, void* stream);
+MOE_API moe_status moe_dequantize_mxfp4_rows(int32_t rows, int32_t K, const void* q, const void* scale, void* out,
+                              void* stream);
+MOE_API moe_status moe_quantize_mxfp4_weights(int32_t batch, int32_t N, int32_t K, const void* w, void* q,
+                              void* scale, void* stream);
 
 /* ------------------------------------------------------------------------ *
  * Status helpers.

@@ -12,7 +12,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG_DIR), "include")
 LIB_NAME = "libmoe.so"
-SOURCES = ["api.cu", "route.cu", "permute.cu", "grouped_gemm.cu", "train.cu", "misc.cu"]
+SOURCES = ["api.cu", "route.cu", "permute.cu", "grouped_gemm.cu", "train.cu", "mxfp4.cu", "misc.cu"]
 
 
 def nvcc_path() -> str:

@@ -4,6 +4,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "mxfp4.cuh"
 #include "train.cuh"
 
 
@@ -235,12 +236,13 @@ moe_status check_ffn(int32_t rows, int32_t H, const moe_ffn_weights* w, const vo
   if (!w || !a) return MOE_ERR_INVALID_ARG;
   if ((need_w13 && !w->w13) || (need_w2 && !w->w2)) return MOE_ERR_INVALID_ARG;
   if (rows < 1 || H < 1 || w->I < 1 || w->groups < 1) return MOE_ERR_INVALID_ARG;
-  if (w->dtype != MOE_BF16 && w->dtype != MOE_E4M3) return MOE_ERR_INVALID_ARG;
+  if (w->dtype != MOE_BF16 && w->dtype != MOE_E4M3 && w->dtype != MOE_MXFP4) return MOE_ERR_INVALID_ARG;
   if (w->tiled != 0 && w->tiled != 1) return MOE_ERR_INVALID_ARG;
   if (w->tiled && w->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (H % 256 != 0 || w->I % 128 != 0 || w->groups > 512) return MOE_ERR_UNSUPPORTED;
+  if (w->dtype != MOE_BF16 && ((need_w13 && !w->w13_scale) || (need_w2 && !w->w2_scale) || !a_scale))
+    return MOE_ERR_INVALID_ARG;
   if (w->dtype == MOE_E4M3) {
-    if ((need_w13 && !w->w13_scale) || (need_w2 && !w->w2_scale) || !a_scale) return MOE_ERR_INVALID_ARG;
     if (H > 8192 || w->I > 8192) return MOE_ERR_UNSUPPORTED;
   }
   if (static_cast<long long>(w->groups) * 2 * w->I > 0x7fffffffLL ||
@@ -357,9 +359,55 @@ moe_status launch_plan(const GemmPlan& p, int epi, cudaStream_t st, int nsm, con
   return check_launch(launch_grouped_gemm(p.fp8, epi, p.tmA, p.tmB, p.g, nsm, st, &two));
 }
 
+// Rows per tile and pipeline stages of the 4-bit GEMMs, by the rows an expert
+// has on average. A small tile leaves room for a fourth stage of weights in
+// flight, which is what counts at a few rows per expert; twice the average, so
+// that most segments still fit one tile and their weights are read once.
+void mx_tile(int32_t rows, int32_t groups, MxGemmArgs* g) {
+  const int32_t twice = 2 * ((rows + groups - 1) / groups);
+  g->bn_max = twice <= 32 ? 32 : twice <= 64 ? 64 : 192;
+  g->stages = g->bn_max <= 64 ? 4 : 3;
+}
+
+// One 4-bit grouped GEMM (scales as moe_quantize_mxfp4_rows / _weights lay them out).
+moe_status run_mx(bool gate_up, int32_t rows, int32_t H, const moe_ffn_weights* w, const void* act, const void* act_scale,
+                  const int32_t* offsets, const float* row_w, void* out, void* out_scale, int32_t* dev_status,
+                  cudaStream_t st, int nsm) {
+  const int32_t I = w->I, K = gate_up ? H : I;
+  const uint64_t a_rows = static_cast<uint64_t>(w->groups) * (gate_up ? 2 * I : H);
+  CUtensorMap tmA;
+  TokenMaps tmB;
+  moe_status s = make_tmap(&tmA, gate_up ? w->w13 : w->w2, true, K / 2, a_rows, gate_up ? 128 : 256);
+  if (s != MOE_OK) return s;
+  for (int i = 0; i < kTokBoxes; ++i)
+    if ((s = make_tmap(&tmB.box[i], act, true, K / 2, rows, 256u >> i)) != MOE_OK) return s;
+  MxGemmArgs g;
+  g.rows = rows;
+  g.K = K;
+  g.groups = w->groups;
+  g.offsets = offsets;
+  g.a_rows_per_group = gate_up ? 2 * I : H;
+  g.n_mblk = gate_up ? I / 128 : H / 256;
+  g.mblk_stride = gate_up ? 128 : 256;
+  g.sub1_off = gate_up ? I : 128;
+  g.a_one_box = gate_up ? 0 : 1;
+  mx_tile(rows, w->groups, &g);
+  g.a_scale = reinterpret_cast<const uint8_t*>(gate_up ? w->w13_scale : w->w2_scale);
+  g.b_scale = static_cast<const uint32_t*>(act_scale);
+  g.row_w = row_w;
+  g.out = out;
+  g.out_ld = gate_up ? I : H;
+  g.out_scale = static_cast<uint8_t*>(out_scale);
+  g.status = dev_status;
+  g.wait_ns = wait_limit();
+  return check_launch(launch_mx_gemm(gate_up, tmA, tmB, g, nsm, st));
+}
+
 moe_status run_gate_up(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* a,
                        const float* a_scale, const int32_t* offsets, void* h_ws, float* h_scale_ws,
                        int32_t* dev_status, cudaStream_t st, int nsm) {
+  if (w->dtype == MOE_MXFP4)
+    return run_mx(true, rows, H, w, a, a_scale, offsets, nullptr, h_ws, h_scale_ws, dev_status, st, nsm);
   GemmPlan p;
   moe_status s = plan_gate_up(rows, H, w, a, a_scale, offsets, h_ws, h_scale_ws, dev_status, &p);
   return s != MOE_OK ? s : launch_plan(p, EPI_SWIGLU, st, nsm);
@@ -368,6 +416,8 @@ moe_status run_gate_up(int32_t rows, int32_t H, const moe_ffn_weights* w, const 
 moe_status run_down(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* h, const float* h_scale,
                     const int32_t* offsets, const float* row_w, void* out, int32_t* dev_status,
                     cudaStream_t st, int nsm) {
+  if (w->dtype == MOE_MXFP4)
+    return run_mx(false, rows, H, w, h, h_scale, offsets, row_w, out, nullptr, dev_status, st, nsm);
   GemmPlan p;
   moe_status s = plan_down(rows, H, w, h, h_scale, offsets, row_w, out, dev_status, &p);
   return s != MOE_OK ? s : launch_plan(p, EPI_WEIGHTED, st, nsm);
@@ -384,7 +434,7 @@ moe_status moe_gate_up_swiglu(int32_t rows, int32_t H, const moe_ffn_weights* w,
   moe_status s = check_ffn(rows, H, w, a, a_scale, true, false);
   if (s != MOE_OK) return s;
   if (!h_ws || (!offsets && w->groups != 1)) return MOE_ERR_INVALID_ARG;
-  if (w->dtype == MOE_E4M3 && !h_scale_ws) return MOE_ERR_INVALID_ARG;
+  if (w->dtype != MOE_BF16 && !h_scale_ws) return MOE_ERR_INVALID_ARG;
   if (any_misaligned(offsets, h_ws, h_scale_ws)) return MOE_ERR_ALIGNMENT;
   int nsm = 0;
   if ((s = sm_count(&nsm)) != MOE_OK) return s;
@@ -479,7 +529,7 @@ moe_status moe_grouped_swiglu(int32_t rows, int32_t H, const moe_ffn_weights* w,
   moe_status s = check_ffn(rows, H, w, a, a_scale, true, true);
   if (s != MOE_OK) return s;
   if (!h_ws || !out || (!offsets && w->groups != 1)) return MOE_ERR_INVALID_ARG;
-  if (w->dtype == MOE_E4M3 && !h_scale_ws) return MOE_ERR_INVALID_ARG;
+  if (w->dtype != MOE_BF16 && !h_scale_ws) return MOE_ERR_INVALID_ARG;
   if (any_misaligned(offsets, row_w, h_ws, h_scale_ws, out)) return MOE_ERR_ALIGNMENT;
   int nsm = 0;
   if ((s = sm_count(&nsm)) != MOE_OK) return s;
@@ -498,11 +548,15 @@ moe_status moe_gate_up_swiglu_with_shared(int32_t rows, int32_t H, const moe_ffn
   if (s != MOE_OK) return s;
   if ((s = check_ffn(sh_rows, H, sw, sh_a, sh_a_scale, true, false)) != MOE_OK) return s;
   if (!offsets || !h_ws || !sh_h_ws || sw->groups != 1 || sw->dtype != w->dtype) return MOE_ERR_INVALID_ARG;
-  if (w->dtype == MOE_E4M3 && (!h_scale_ws || !sh_h_scale_ws)) return MOE_ERR_INVALID_ARG;
+  if (w->dtype != MOE_BF16 && (!h_scale_ws || !sh_h_scale_ws)) return MOE_ERR_INVALID_ARG;
   if (any_misaligned(offsets, h_ws, h_scale_ws, sh_h_ws, sh_h_scale_ws)) return MOE_ERR_ALIGNMENT;
   int nsm = 0;
   if ((s = sm_count(&nsm)) != MOE_OK) return s;
   cudaStream_t st = as_stream(stream);
+  if (w->dtype == MOE_MXFP4) {
+    s = run_gate_up(rows, H, w, a, a_scale, offsets, h_ws, h_scale_ws, dev_status, st, nsm);
+    return s != MOE_OK ? s : run_gate_up(sh_rows, H, sw, sh_a, sh_a_scale, nullptr, sh_h_ws, sh_h_scale_ws, dev_status, st, nsm);
+  }
   GemmPlan p, q;
   if ((s = plan_gate_up(rows, H, w, a, a_scale, offsets, h_ws, h_scale_ws, dev_status, &p)) != MOE_OK) return s;
   if ((s = plan_gate_up(sh_rows, H, sw, sh_a, sh_a_scale, nullptr, sh_h_ws, sh_h_scale_ws, dev_status, &q)) !=
@@ -523,6 +577,10 @@ moe_status moe_down_proj_with_shared(int32_t rows, int32_t H, const moe_ffn_weig
   int nsm = 0;
   if ((s = sm_count(&nsm)) != MOE_OK) return s;
   cudaStream_t st = as_stream(stream);
+  if (w->dtype == MOE_MXFP4) {
+    s = run_down(rows, H, w, h, h_scale, offsets, row_w, out, dev_status, st, nsm);
+    return s != MOE_OK ? s : run_down(sh_rows, H, sw, sh_h, sh_h_scale, nullptr, nullptr, sh_out, dev_status, st, nsm);
+  }
   GemmPlan p, q;
   if ((s = plan_down(rows, H, w, h, h_scale, offsets, row_w, out, dev_status, &p)) != MOE_OK) return s;
   if ((s = plan_down(sh_rows, H, sw, sh_h, sh_h_scale, nullptr, nullptr, sh_out, dev_status, &q)) != MOE_OK)
@@ -923,6 +981,29 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
     s = check_launch(launch_wgrad(q, nsm, st));
   }
   return s;
+}
+
+moe_status moe_quantize_mxfp4_rows(int32_t rows, int32_t K, const void* a, int32_t a_rows, const int32_t* src_rows, void* q,
+                                   void* scale, int32_t* dev_status, void* stream) {
+  if (rows < 1 || K < 1 || a_rows < 1 || !a || !q || !scale || (!src_rows && a_rows < rows)) return MOE_ERR_INVALID_ARG;
+  if (K % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (any_misaligned(a, src_rows, q, scale)) return MOE_ERR_ALIGNMENT;
+  return check_launch(launch_mx_quant_rows(rows, K, a, a_rows, src_rows, q, scale, dev_status, as_stream(stream)));
+}
+
+moe_status moe_dequantize_mxfp4_rows(int32_t rows, int32_t K, const void* q, const void* scale, void* out, void* stream) {
+  if (rows < 1 || K < 1 || !q || !scale || !out) return MOE_ERR_INVALID_ARG;
+  if (K % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (any_misaligned(q, scale, out)) return MOE_ERR_ALIGNMENT;
+  return check_launch(launch_mx_dequant_rows(rows, K, q, scale, out, as_stream(stream)));
+}
+
+moe_status moe_quantize_mxfp4_weights(int32_t batch, int32_t N, int32_t K, const void* w, void* q, void* scale,
+                                      void* stream) {
+  if (batch < 1 || N < 1 || K < 1 || !w || !q || !scale) return MOE_ERR_INVALID_ARG;
+  if (N % 128 != 0 || K % 128 != 0 || static_cast<long long>(batch) * N > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  if (any_misaligned(w, q, scale)) return MOE_ERR_ALIGNMENT;
+  return check_launch(launch_mx_quant_weights(batch, N, K, w, q, scale, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,530 @@
+// Microscaled 4-bit floating point (MXFP4): E2M1 values (0, 0.5, 1, 1.5, 2, 3,
+// 4, 6 and their negatives, two a byte, the first in the low half) with one
+// E8M0 scale 2^(s - 127) per 32 consecutive values.
+//
+// Quantising a block: s - 127 = floor(log2 amax) - 2, clamped to [-127, 125]
+// (2 is the exponent of the largest code, 6 = 1.5 * 2^2), s = 127 for a block
+// of zeros; code = nearest of v / scale, ties to the even code, above 6 to 6.
+// The division is by a power of two and so exact: codes depend on nothing but
+// this definition. A block holding NaN or infinity gets s = 255 (NaN), which
+// makes every product with it NaN.
+//
+// The product runs on the tensor cores' block-scaled form
+// (tcgen05.mma kind::mxf4, K = 64 and two scales per row and instruction): the
+// scales are applied inside the MMA, sums are fp32 in TMEM.
+#include "mxfp4.cuh"
+
+#include "segments.cuh"
+
+namespace moe {
+
+// ---------------------------------------------------------------- values
+__device__ __forceinline__ uint32_t mx_scale_of(float amax) {
+  const int field = static_cast<int>(__float_as_uint(amax) >> 23);   // amax >= 0; NaN and infinity: 255
+  if (field == 255) return 255u;
+  if (amax == 0.0f) return 127u;
+  const int e = field - 127 - 2;                                     // subnormal: below the clamp as well
+  return static_cast<uint32_t>(max(e, -127) + 127);
+}
+// 1 / scale as a float: exact (a NaN scale's blocks quantise against 1)
+__device__ __forceinline__ float mx_inv_scale(uint32_t s) {
+  return s == 255u ? 1.0f : __uint_as_float((254u - s) << 23);       // s <= 252
+}
+// eight values -> eight codes, value i in bits 4i..4i+3
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float inv) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0] * inv), "f"(v[1] * inv), "f"(v[2] * inv), "f"(v[3] * inv), "f"(v[4] * inv), "f"(v[5] * inv),
+        "f"(v[6] * inv), "f"(v[7] * inv));
+  return r;
+}
+// |v|, with NaN as infinity, so that a maximum over a block keeps either
+__device__ __forceinline__ float mx_mag(float v) { return v != v ? INFINITY : fabsf(v); }
+
+__device__ __forceinline__ void bf16x8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// Four lanes hold a block of 32 values, eight each: its scale byte and this
+// lane's codes.
+__device__ __forceinline__ uint32_t mx_block(const uint4& u, uint32_t& scale) {
+  float f[8];
+  bf16x8(u, f);
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, mx_mag(f[i]));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  scale = mx_scale_of(m);
+  return mx_codes8(f, mx_inv_scale(scale));
+}
+
+// ---------------------------------------------------------------- rows
+// One warp per row, 256 values a step (16 bytes read, 4 written per lane), the
+// scale bytes gathered into the words [K / 128][rows]. Bound by HBM: 2 bytes
+// read and 0.53 written per value.
+constexpr int kMxRows = 8;                                           // rows (warps) per CTA
+__global__ void __launch_bounds__(32 * kMxRows)
+mx_quant_rows_kernel(int rows, int K, const uint4* __restrict__ a, int a_rows, const int32_t* __restrict__ src,
+                     uint32_t* __restrict__ q, uint32_t* __restrict__ scale, int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x * kMxRows + (threadIdx.x >> 5);
+  if (r >= rows) return;                                             // warp-uniform
+  int from = src ? src[r] : r;
+  const bool bad = from < 0 || from >= a_rows;
+  if (bad) {                                                         // such a row becomes zeros
+    if (lane == 0) flag_status(status, MOE_DEVSTAT_BAD_EXPERT_ID);
+    from = 0;
+  }
+  const uint4* row = a + static_cast<size_t>(from) * (K / 8);
+  uint32_t* qr = q + static_cast<size_t>(r) * (K / 8);
+  constexpr int U = 4;                                               // steps in flight
+  for (int c0 = 0; c0 < K / 8; c0 += 32 * U) {
+    uint4 u[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + 32 * i + lane;
+      u[i] = c < K / 8 && !bad ? row[c] : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + 32 * i + lane;
+      uint32_t s;
+      const uint32_t codes = mx_block(u[i], s);
+      // the four blocks of 128 values: lanes 0, 4, 8, 12 and 16, 20, 24, 28
+      uint32_t w = s << (8 * ((lane >> 2) & 3));
+      w |= __shfl_xor_sync(0xffffffffu, w, 4);
+      w |= __shfl_xor_sync(0xffffffffu, w, 8);
+      if (c < K / 8) {
+        qr[c] = codes;
+        if ((lane & 15) == 0) scale[static_cast<size_t>(c / 16) * rows + r] = w;
+      }
+    }
+  }
+}
+
+// The values the codes stand for, in bf16 (exact: two significant bits, and
+// 2^-128 .. 1.5 * 2^127 are bf16 numbers).
+__device__ __forceinline__ uint32_t mx_bf16x2(uint32_t codes, float sc) {
+  // E2M1 magnitude m: 0, 0.5, 1, 1.5, 2, 3, 4, 6
+  auto value = [&](uint32_t c) {
+    const uint32_t m = c & 7u;
+    const float x = m < 2 ? 0.5f * static_cast<float>(m) : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
+    return (c & 8u) ? -x * sc : x * sc;
+  };
+  const __nv_bfloat162 h = __floats2bfloat162_rn(value(codes & 15u), value((codes >> 4) & 15u));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__global__ void __launch_bounds__(32 * kMxRows)
+mx_dequant_rows_kernel(int rows, int K, const uint32_t* __restrict__ q, const uint32_t* __restrict__ scale,
+                       uint4* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x * kMxRows + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const uint32_t* qr = q + static_cast<size_t>(r) * (K / 8);
+  uint4* o = out + static_cast<size_t>(r) * (K / 8);
+  constexpr int U = 4;
+  for (int c0 = 0; c0 < K / 8; c0 += 32 * U) {
+    uint32_t code[U], w[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + 32 * i + lane;
+      code[i] = c < K / 8 ? qr[c] : 0u;
+      w[i] = c < K / 8 ? scale[static_cast<size_t>(c / 16) * rows + r] : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + 32 * i + lane;
+      const uint32_t s = (w[i] >> (8 * ((lane >> 2) & 3))) & 255u;
+      // 2^(s - 127): s = 0 is the subnormal 2^-127, s = 255 NaN
+      const float sc = s == 255u ? __uint_as_float(0x7fc00000u) : s == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(s << 23);
+      uint4 v;
+      v.x = mx_bf16x2(code[i], sc);
+      v.y = mx_bf16x2(code[i] >> 8, sc);
+      v.z = mx_bf16x2(code[i] >> 16, sc);
+      v.w = mx_bf16x2(code[i] >> 24, sc);
+      if (c < K / 8) o[c] = v;
+    }
+  }
+}
+
+// Weights (once, when a layer is built): one warp per row; scales in the order
+// the GEMM copies into shared memory, per 128 rows x 128 columns row r's word
+// at (r % 32) * 16 + (r / 32) * 4.
+__global__ void __launch_bounds__(256)
+mx_quant_weights_kernel(long long n_rows, int N, int K, const uint4* __restrict__ w, uint32_t* __restrict__ q,
+                        uint8_t* __restrict__ scale) {
+  const int lane = threadIdx.x & 31;
+  const long long gr = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (gr >= n_rows) return;
+  const int rr = static_cast<int>(gr % 128);
+  uint32_t* sc = reinterpret_cast<uint32_t*>(scale + (gr / 128) * static_cast<size_t>(K / 128) * 512 + (rr % 32) * 16 +
+                                             (rr / 32) * 4);
+  for (int c0 = 0; c0 < K / 8; c0 += 32) {
+    const int c = c0 + lane;
+    uint32_t s;
+    const uint32_t codes = mx_block(c < K / 8 ? w[gr * (K / 8) + c] : make_uint4(0u, 0u, 0u, 0u), s);
+    uint32_t word = s << (8 * ((lane >> 2) & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+    if (c < K / 8) {
+      q[gr * (K / 8) + c] = codes;
+      if ((lane & 15) == 0) sc[static_cast<size_t>(c / 16) * 128] = word;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- product
+// 32 rows x 16 bytes of shared memory into 4 TMEM columns, all lane quarters.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem_addr) {
+  // no swizzle, groups of 8 rows 128 B apart
+  const uint64_t d = static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1u) << 16 |
+                     static_cast<uint64_t>(128u >> 4) << 32 | static_cast<uint64_t>(1u) << 46;
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor, kind::mxf4: E2M1 x E2M1 (1 at bits 7 and 10), N / 8 at
+// 17, UE8M0 scales (bit 23), M / 128 at 27; the scale pair used (bytes 0-1 or
+// 2-3 of a row's word) at bits 4 (B) and 29 (A).
+__device__ __forceinline__ uint32_t mxf4_idesc(uint32_t M, uint32_t N, uint32_t pair) {
+  return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 7) << 27) | ((2 * pair) << 4) | ((2 * pair) << 29);
+}
+
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+constexpr int kMxEpi = 8;                                            // epilogue warps
+constexpr int kMxThreads = 32 * (4 + kMxEpi);
+constexpr int kMxMaxStages = 4;
+constexpr uint32_t kMxA = 256 * 128;                                 // 256 weight rows x 256 values
+constexpr uint32_t kMxSfa = 2048, kMxSfb = 2048;
+__host__ __device__ constexpr uint32_t mx_stage_bytes(int bn) { return kMxA + static_cast<uint32_t>(bn) * 128u + kMxSfa + kMxSfb; }
+
+// Tiles as in the forward GEMMs: 256 weight rows (gate and up rows of 128
+// features, or 256 rows of w2) as the MMA's A, up to bn_max rows of a segment
+// as B, accumulated side by side in TMEM columns [0, bn) and [bn, 2 bn). A
+// stage is 256 values of K: the codes by TMA, the weights' scales as one or two
+// 512-byte blocks per 128 rows by a bulk copy, and the rows' scales, which lie
+// row by row at any offset, arranged the same way by warp 2. The MMA thread
+// copies the scales to TMEM columns of the stage's own (2 bn + 32 * stage ...),
+// so no copy meets MMAs still reading the last ones.
+//   warp 0 TMA, warp 1 TMEM and MMAs, warp 2 the rows' scales, warps 4..11 the
+//   epilogue: gate/up quantises h = SiLU(g) u, a warp's 32 features being one
+//   block of 32, through a shared tile so that a lane has one row's block.
+// At a few rows per expert the weights' bytes bound it (4.25 bits a value).
+template <bool GATE_UP>
+__global__ void __launch_bounds__(kMxThreads, 1)
+mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ TokenMaps tmB, const MxGemmArgs a) {
+  extern __shared__ __align__(1024) uint8_t dsmem[];
+  __shared__ SegSched sched;
+  __shared__ __align__(16) float tile_s[kMxEpi][32 * 33];
+  __shared__ uint64_t full_bar[kMxMaxStages], empty_bar[kMxMaxStages];
+  __shared__ uint64_t tmem_full, tmem_empty, drain_bar;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int issued_parity[kMxMaxStages], scaled_parity[kMxMaxStages];   // last phase of the loads', of warp 2's arrival
+  __shared__ volatile int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
+  const uint32_t bn = static_cast<uint32_t>(a.bn_max);
+  const uint32_t stage_bytes = mx_stage_bytes(a.bn_max);
+  const int stages = a.stages;
+  auto sA = [&](int st) { return smem + st * stage_bytes; };
+  auto sB = [&](int st) { return smem + st * stage_bytes + kMxA; };
+  auto sSfa = [&](int st) { return smem + st * stage_bytes + kMxA + bn * 128u; };
+  auto sSfb = [&](int st) { return smem + st * stage_bytes + kMxA + bn * 128u + kMxSfa; };
+  const SegProblem sp{a.rows, a.groups, a.offsets, a.n_mblk, a.bn_max, a.status};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMxMaxStages; ++i) {
+      mbar_init(&full_bar[i], 2);                                    // the loads' and warp 2's
+      mbar_init(&empty_bar[i], 1);
+      issued_parity[i] = scaled_parity[i] = -1;
+    }
+    mbar_init(&tmem_full, 1);
+    mbar_init(&tmem_empty, 32 * kMxEpi);
+    mbar_init(&drain_bar, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    for (int i = 0; i < kTokBoxes; ++i) tma_prefetch_desc(&tmB.box[i]);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base_s, 512);
+    tmem_relinquish();
+  }
+  if (warp == 3) build_schedule(sched, sp, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_s;
+  const int total = sched.tile_start[a.groups];
+  const int k128 = a.K / 128;                                        // blocks of 128 values
+  const int nk = (k128 + 1) / 2;                                     // stages per tile
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol_once = policy_evict_first();
+      const uint64_t pol_reuse = policy_evict_normal();
+      const uint64_t pol_x = policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x) {
+        const SegTile ti = decode_tile(sched, sp, t);
+        const int row0 = ti.g * a.a_rows_per_group + ti.mb * a.mblk_stride;
+        const int row1 = row0 + a.sub1_off;
+        const uint8_t* sf0 = a.a_scale + static_cast<size_t>(row0 / 128) * k128 * 512;
+        const uint8_t* sf1 = a.a_scale + static_cast<size_t>(row1 / 128) * k128 * 512;
+        const uint64_t pol_w = ti.ntb > 1 ? pol_reuse : pol_once;
+        bool ok = true;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag, a.status, a.wait_ns)) { ok = false; break; }
+          uint64_t* fb = &full_bar[stage];
+          const uint32_t sf_bytes = k128 - 2 * kb >= 2 ? 1024u : 512u;
+          mbar_arrive_expect_tx(fb, kMxA + static_cast<uint32_t>(ti.N) * 128u + 2 * sf_bytes);
+          tma_load_2d(sA(stage), &tmA, fb, kb * 128, row0, pol_w);
+          if (!a.a_one_box) tma_load_2d(sA(stage) + 128 * 128, &tmA, fb, kb * 128, row1, pol_w);
+          uint8_t* bdst = sB(stage);
+          load_token_rows(ti.N, [&](int which, int off) {
+            tma_load_2d(bdst + off * 128, &tmB.box[which], fb, kb * 128, ti.row0 + off, pol_x);
+          });
+          bulk_load(sSfa(stage), sf0 + kb * 1024, sf_bytes, fb);
+          bulk_load(sSfa(stage) + 1024, sf1 + kb * 1024, sf_bytes, fb);
+          issued_parity[stage] = static_cast<int>(phase);
+          if (++stage == stages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+      }
+    }
+  } else if (warp == 2) {
+    // the rows' scales: word of row r and block kk at b_scale[kk * rows + r],
+    // to (r % 32) * 16 + (r / 32 % 4) * 4 of a 512-byte block per 128 rows
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < total && ok && !abort_flag; t += gridDim.x) {
+      const SegTile ti = decode_tile(sched, sp, t);
+      const int nrb = (ti.N + 127) / 128;
+      uint32_t w[2][2][4];
+      auto fetch = [&](int kb) {
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh)
+#pragma unroll
+          for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int r = rb * 128 + c * 32 + lane;                // rows behind the tile's: scale 1, not used
+              w[kh][rb][c] = r < ti.n_valid && 2 * kb + kh < k128
+                                 ? __ldg(a.b_scale + static_cast<size_t>(2 * kb + kh) * a.rows + ti.row0 + r) : 0x7f7f7f7fu;
+            }
+      };
+      fetch(0);
+      for (int kb = 0; kb < nk; ++kb) {
+        if (lane == 0) ok = mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag, a.status, a.wait_ns);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        uint8_t* dst = sSfb(stage);
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh)
+#pragma unroll
+          for (int rb = 0; rb < 2; ++rb)
+            if (rb < nrb)
+              *reinterpret_cast<uint4*>(dst + (kh * 2 + rb) * 512 + lane * 16) =
+                  make_uint4(w[kh][rb][0], w[kh][rb][1], w[kh][rb][2], w[kh][rb][3]);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          scaled_parity[stage] = static_cast<int>(phase);
+          mbar_arrive(&full_bar[stage]);
+        }
+        if (kb + 1 < nk) fetch(kb + 1);
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, it = 0;
+      for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x, ++it) {
+        const SegTile ti = decode_tile(sched, sp, t);
+        const uint32_t id0 = mxf4_idesc(128u, static_cast<uint32_t>(ti.N), 0u);
+        const uint32_t id1 = mxf4_idesc(128u, static_cast<uint32_t>(ti.N), 1u);
+        const bool wide = ti.N > 128;
+        if (!mbar_wait(&tmem_empty, (it & 1u) ^ 1u, &abort_flag, a.status, a.wait_ns)) break;
+        tc_fence_after();
+        bool ok = true;
+        uint32_t acc = 0;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!mbar_wait(&full_bar[stage], phase, &abort_flag, a.status, a.wait_ns)) { ok = false; break; }
+          tc_fence_after();
+          const int halves = min(2, k128 - 2 * kb);
+          const uint32_t sf = tmem_base + 2 * bn + 32u * stage;      // [A0: 8][A1: 8][B: 16] columns
+          const uint32_t s_a = smem_u32(sSfa(stage)), s_b = smem_u32(sSfb(stage));
+          const uint64_t ad = sw128_desc(smem_u32(sA(stage))), bd = sw128_desc(smem_u32(sB(stage)));
+          for (int kh = 0; kh < halves; ++kh) {
+            tmem_copy_scales(sf + kh * 4, s_a + kh * 512);
+            tmem_copy_scales(sf + 8 + kh * 4, s_a + 1024 + kh * 512);
+            tmem_copy_scales(sf + 16 + kh * 8, s_b + kh * 1024);
+            if (wide) tmem_copy_scales(sf + 16 + kh * 8 + 4, s_b + kh * 1024 + 512);
+          }
+          for (int kh = 0; kh < halves; ++kh) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {                            // 64 values: 32 B, 2 descriptor units
+              const uint64_t k = static_cast<uint64_t>(2 * (2 * kh + p));
+              const uint32_t id = p ? id1 : id0;
+              umma_mxf4(tmem_base, ad + k, bd + k, id, sf + kh * 4, sf + 16 + kh * 8, acc);
+              umma_mxf4(tmem_base + bn, ad + (128 * 128 >> 4) + k, bd + k, id, sf + 8 + kh * 4, sf + 16 + kh * 8, acc);
+              acc = 1;
+            }
+          }
+          umma_commit(&empty_bar[stage]);
+          if (++stage == stages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        umma_commit(&tmem_full);
+      }
+      umma_commit(&drain_bar);   // all issued MMAs must finish before TMEM is released
+      mbar_wait_drain(&drain_bar, 0);
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3;
+    const int c0 = (warp - 4) / 4;
+    constexpr int cstep = kMxEpi / 4;
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    float* ts = tile_s[warp - 4];
+    uint32_t it = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
+      const SegTile ti = decode_tile(sched, sp, t);
+      const int nchunk = (ti.N + 31) / 32;
+      if (!mbar_wait(&tmem_full, it & 1u, &abort_flag, a.status, a.wait_ns)) break;
+      tc_fence_after();
+      if (GATE_UP) {
+        uint8_t* out = reinterpret_cast<uint8_t*>(a.out);
+        for (int c = c0; c < nchunk; c += cstep) {
+          float g[32], u[32];
+          tmem_ld32(lane_addr + c * 32, g);
+          tmem_ld32(lane_addr + bn + c * 32, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) ts[j * 33 + lane] = silu(g[j]) * u[j];
+          __syncwarp();
+          // lane = row: its 32 features of this warp are one block
+          float m = 0.0f;
+#pragma unroll
+          for (int f = 0; f < 32; ++f) {
+            g[f] = ts[lane * 33 + f];
+            m = fmaxf(m, mx_mag(g[f]));
+          }
+          const uint32_t s = mx_scale_of(m);
+          const float inv = mx_inv_scale(s);
+          uint32_t code[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = g[8 * i + e];
+            code[i] = mx_codes8(v, inv);
+          }
+          const int r = c * 32 + lane;
+          if (r < ti.n_valid) {
+            const size_t row = static_cast<size_t>(ti.row0 + r);
+            *reinterpret_cast<uint4*>(out + row * (a.out_ld / 2) + ti.mb * 64 + q * 16) =
+                make_uint4(code[0], code[1], code[2], code[3]);
+            a.out_scale[(static_cast<size_t>(ti.mb) * a.rows + row) * 4 + q] = static_cast<uint8_t>(s);
+          }
+          __syncwarp();
+        }
+      } else {
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
+        __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(ts);
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          for (int c = c0; c < nchunk; c += cstep) {
+            const int r = c * 32 + lane;
+            const float wl = a.row_w && r < ti.n_valid ? __ldg(a.row_w + ti.row0 + r) : 1.0f;
+            float v[32];
+            tmem_ld32(lane_addr + s * bn + c * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= __shfl_sync(0xffffffffu, wl, j);
+            store_tile<32>(stg, v, lane, out, static_cast<size_t>(a.out_ld), ti.row0 + c * 32, ti.n_valid - c * 32,
+                           ti.mb * 256 + s * 128 + 32 * q);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&tmem_empty);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // after an abort every copy issued lands before the CTA leaves; where warp 2
+  // has not arrived on the stage, this thread does
+  if (abort_flag && warp == 0 && lane == 0) {
+    for (int i = 0; i < kMxMaxStages; ++i) {
+      if (issued_parity[i] < 0) continue;
+      if (scaled_parity[i] != issued_parity[i]) mbar_arrive(&full_bar[i]);
+      mbar_wait_drain(&full_bar[i], static_cast<uint32_t>(issued_parity[i]));
+    }
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem_base, 512);
+}
+
+// ---------------------------------------------------------------- launches
+cudaError_t launch_mx_gemm(bool gate_up, const CUtensorMap& tmA, const TokenMaps& tmB, const MxGemmArgs& a, int grid,
+                           cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(a.stages) * mx_stage_bytes(a.bn_max) + 1024;
+  auto kern = gate_up ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kMxThreads, smem, stream>>>(tmA, tmB, a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_mx_quant_rows(int rows, int K, const void* a, int a_rows, const int32_t* src, void* q, void* scale,
+                                 int32_t* status, cudaStream_t stream) {
+  mx_quant_rows_kernel<<<(rows + kMxRows - 1) / kMxRows, 32 * kMxRows, 0, stream>>>(
+      rows, K, static_cast<const uint4*>(a), a_rows, src, static_cast<uint32_t*>(q), static_cast<uint32_t*>(scale), status);
+  return cudaGetLastError();
+}
+cudaError_t launch_mx_dequant_rows(int rows, int K, const void* q, const void* scale, void* out, cudaStream_t stream) {
+  mx_dequant_rows_kernel<<<(rows + kMxRows - 1) / kMxRows, 32 * kMxRows, 0, stream>>>(
+      rows, K, static_cast<const uint32_t*>(q), static_cast<const uint32_t*>(scale), static_cast<uint4*>(out));
+  return cudaGetLastError();
+}
+cudaError_t launch_mx_quant_weights(int batch, int N, int K, const void* w, void* q, void* scale, cudaStream_t stream) {
+  const long long n = static_cast<long long>(batch) * N;
+  mx_quant_weights_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, stream>>>(
+      n, N, K, static_cast<const uint4*>(w), static_cast<uint32_t*>(q), static_cast<uint8_t*>(scale));
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -22,7 +22,7 @@ MOE_ERR_DEVICE_CHECK = 5
 MOE_ERR_DEVICE_TIMEOUT = 6
 MOE_DEVSTAT_BAD_EXPERT_ID = 0x1
 MOE_DEVSTAT_TIMEOUT = 0x2
-MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_E4M3, MOE_MXFP4 = 0, 1, 2, 3
 MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 
 EXPORTED = [
@@ -34,6 +34,7 @@ EXPORTED = [
     "moe_combine", "moe_bias_update", "moe_aux_loss_workspace_size", "moe_aux_loss",
     "moe_gate_up_swiglu_train", "moe_swiglu_ffn_backward_workspace_size", "moe_swiglu_ffn_backward",
     "moe_route_backward", "moe_gate_backward",
+    "moe_quantize_mxfp4_rows", "moe_dequantize_mxfp4_rows", "moe_quantize_mxfp4_weights",
     "moe_quantize_blocks", "moe_quantize_rows",
     "moe_read_device_status", "moe_last_cuda_error", "moe_status_string", "moe_abi_version",
     "moe_set_wait_limit_ns", "moe_wait_limit_ns",
@@ -107,6 +108,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                     _P, _P, ctypes.c_size_t, _P, _P],
         "moe_route_backward": [_I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P],
         "moe_gate_backward": [_I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P],
+        "moe_quantize_mxfp4_rows": [_I, _I, _P, _I, _P, _P, _P, _P, _P],
+        "moe_dequantize_mxfp4_rows": [_I, _I, _P, _P, _P, _P],
+        "moe_quantize_mxfp4_weights": [_I, _I, _I, _P, _P, _P, _P],
         "moe_quantize_blocks": [_I, _I, _I, _P, _P, _P, _P],
         "moe_quantize_rows": [_I, _I, _P, _P, _P, _P],
         "moe_read_device_status": [_P, ctypes.POINTER(ctypes.c_int32), _P],
@@ -406,6 +410,35 @@ def moe_quantize_blocks(batch, N, K, w, q, scale, stream=None):
 def moe_quantize_rows(M, K, a, q, scale, stream=None):
     _check("moe_quantize_rows", load_library().moe_quantize_rows(
         M, K, _ptr(a), _ptr(q), _ptr(scale), _stream(stream)))
+
+
+def moe_quantize_mxfp4_rows(rows, K, a, a_rows, src_rows, q, scale, dev_status=None, stream=None):
+    """Rows src_rows of a (None: its first rows) as 4-bit codes q [rows, K/2]
+    (uint8) and scales [K/128, rows, 4] (uint8)."""
+    u8 = torch.uint8
+    _expect("moe_quantize_mxfp4_rows", a=(a, a_rows * K, torch.bfloat16), src_rows=(src_rows, rows, torch.int32),
+            q=(q, rows * K // 2, u8), scale=(scale, rows * K // 32, u8))
+    _check("moe_quantize_mxfp4_rows", load_library().moe_quantize_mxfp4_rows(
+        rows, K, _ptr(a), a_rows, _ptr(src_rows), _ptr(q), _ptr(scale), _ptr(dev_status), _stream(stream)))
+
+
+def moe_dequantize_mxfp4_rows(rows, K, q, scale, out, stream=None):
+    """The bf16 values of moe_quantize_mxfp4_rows' codes."""
+    u8 = torch.uint8
+    _expect("moe_dequantize_mxfp4_rows", q=(q, rows * K // 2, u8), scale=(scale, rows * K // 32, u8),
+            out=(out, rows * K, torch.bfloat16))
+    _check("moe_dequantize_mxfp4_rows", load_library().moe_dequantize_mxfp4_rows(
+        rows, K, _ptr(q), _ptr(scale), _ptr(out), _stream(stream)))
+
+
+def moe_quantize_mxfp4_weights(batch, N, K, w, q, scale, stream=None):
+    """Weights w [batch, N, K] as codes q [batch, N, K/2] and scales
+    [batch, N/128, K/128, 512] (uint8), as the MOE_MXFP4 products take them."""
+    u8 = torch.uint8
+    _expect("moe_quantize_mxfp4_weights", w=(w, batch * N * K, torch.bfloat16), q=(q, batch * N * K // 2, u8),
+            scale=(scale, batch * N * K // 32, u8))
+    _check("moe_quantize_mxfp4_weights", load_library().moe_quantize_mxfp4_weights(
+        batch, N, K, _ptr(w), _ptr(q), _ptr(scale), _stream(stream)))
 
 
 def moe_read_device_status(dev_status, stream=None) -> int:
