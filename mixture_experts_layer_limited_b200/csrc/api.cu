@@ -82,6 +82,53 @@ moe_status make_token_tmaps(TokenMaps* m, const void* ptr, bool fp8, uint64_t K,
   return MOE_OK;
 }
 
+// A 3-D bf16 tensor map with 128-byte swizzle; strides in bytes.
+moe_status make_tmap_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
+                        uint32_t b1, uint32_t b2) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {s1, s2};
+  cuuint32_t box[3] = {64, b1, b2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
+  return MOE_OK;
+}
+
+// A row-major bf16 matrix [rows, cols] as [cols / 64] blocks of [rows, 64];
+// boxes of 64 rows of `blocks` blocks.
+moe_status make_block_tmap(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint32_t blocks = 2) {
+  return make_tmap_3d(m, ptr, 64, rows, cols / 64, cols * 2, 128, 64, blocks);
+}
+
+// A weight as train_gemm_kernel loads it, one box per block of 64 K:
+//   forward (w13 [groups, 2, I, H]): 128 gate rows and the same features' up
+//     rows; tiled: one 256-row block.
+//   else ([groups, K, M] or its tiled copy, K blocks of 256 rows): 64 K rows x
+//     128 * subs features, as column blocks of 64.
+moe_status make_train_weight_tmap(CUtensorMap* m, const void* w, int mode, int tiled, int64_t groups, int64_t K, int64_t M,
+                                  int subs) {
+  if (tiled) {
+    const uint64_t values = static_cast<uint64_t>(groups) * K * M * (mode == TRAIN_FORWARD ? 2 : 1);
+    return make_tmap_3d(m, w, 64, 256, values / (64 * 256), 128, 256 * 128, mode == TRAIN_FORWARD ? 256 : 64,
+                        mode == TRAIN_FORWARD ? 1 : 2 * subs);
+  }
+  if (mode == TRAIN_FORWARD) return make_tmap_3d(m, w, K, M, 2 * groups, K * 2, K * 2 * M, 128, 2);
+  return make_block_tmap(m, w, M, groups * K, 2 * subs);
+}
+
+// Token-row maps of a CTA pair: one box for each half tile of 16, 32, .. 128 rows.
+moe_status make_half_tmaps(HalfMaps* m, const void* ptr, uint64_t K, uint64_t rows) {
+  for (int i = 0; i < 8; ++i) {
+    moe_status s = make_tmap(&m->box[i], ptr, false, K, rows, 16 * (i + 1));
+    if (s != MOE_OK) return s;
+  }
+  return MOE_OK;
+}
+
 moe_status sm_count(int* n) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -491,24 +538,22 @@ moe_status moe_gate_up_swiglu_train(int32_t rows, int32_t H, const moe_ffn_weigh
   if ((s = sm_count(&nsm)) != MOE_OK) return s;
   const int I = w->I;
   CUtensorMap tmA;
-  TokenMaps tmB;
-  s = w->tiled ? make_tmap(&tmA, w->w13, false, 64, static_cast<uint64_t>(w->groups) * 2 * I * (H / 64), 256)
-               : make_tmap(&tmA, w->w13, false, H, static_cast<uint64_t>(w->groups) * 2 * I, 128);
+  HalfMaps tmB;
+  s = make_train_weight_tmap(&tmA, w->w13, TRAIN_FORWARD, w->tiled, w->groups, H, I, 2);
   if (s != MOE_OK) return s;
-  if ((s = make_token_tmaps(&tmB, a, false, H, rows)) != MOE_OK) return s;
+  if ((s = make_half_tmaps(&tmB, a, H, rows)) != MOE_OK) return s;
   TrainGemmArgs g;
   g.rows = rows;
   g.K = H;
   g.M = I;
   g.groups = w->groups;
   g.offsets = offsets;
-  g.n_mblk = I / 128;
   g.tiled = w->tiled;
   g.gu = static_cast<__nv_bfloat16*>(gu);
   g.h = static_cast<__nv_bfloat16*>(h);
   g.status = dev_status;
   g.wait_ns = wait_limit();
-  return check_launch(launch_train_gemm(TRAIN_FORWARD, tmA, tmB, g, nsm, as_stream(stream)));
+  return check_launch(launch_train_gemm(TRAIN_FORWARD, 2, tmA, tmB, g, nsm, as_stream(stream)));
 }
 
 moe_status moe_down_proj(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* h, const float* h_scale,
@@ -777,22 +822,6 @@ moe_status make_out_tmap(CUtensorMap* m, const void* ptr, bool f32, uint64_t inn
   return MOE_OK;
 }
 
-// A row-major bf16 matrix [rows, cols] as [cols / 64] blocks of [rows, 64];
-// boxes of 64 rows of two blocks.
-moe_status make_block_tmap(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows) {
-  EncodeTiledFn enc = encode_tiled();
-  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
-  cuuint64_t dims[3] = {64, rows, cols / 64};
-  cuuint64_t strides[2] = {cols * 2, 128};
-  cuuint32_t box[3] = {64, 64, 2};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
-  return MOE_OK;
-}
-
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // Parts of moe_swiglu_ffn_backward's workspace.
@@ -820,7 +849,8 @@ moe_status plan_wgrad(WgradProblem* p, int32_t rows, int32_t groups, const void*
   p->M = M;
   p->N = N;
   p->n_blocks = (N + 255) / 256;
-  p->per_group = (M + 255) / 256 * p->n_blocks;
+  p->m_blocks = (M + 255) / 256;
+  p->per_group = p->m_blocks * p->n_blocks;
   p->tiles = groups * p->per_group;
   return MOE_OK;
 }
@@ -867,18 +897,16 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
 
   // dh0 = d_out w2 and the activation's backward: d_gu, row_w * h, partial sums of d_row_w
   CUtensorMap tmA;
-  TokenMaps tmB;
-  s = w->tiled ? make_tmap(&tmA, w->w2, false, 64, static_cast<uint64_t>(w->groups) * H * (I / 64), 64)
-               : make_tmap(&tmA, w->w2, false, I, static_cast<uint64_t>(w->groups) * H, 64);
+  HalfMaps tmB;
+  s = make_train_weight_tmap(&tmA, w->w2, TRAIN_HIDDEN, w->tiled, w->groups, H, I, 1);
   if (s != MOE_OK) return s;
-  if ((s = make_token_tmaps(&tmB, d_out, false, H, rows)) != MOE_OK) return s;
+  if ((s = make_half_tmaps(&tmB, d_out, H, rows)) != MOE_OK) return s;
   TrainGemmArgs g;
   g.rows = rows;
   g.K = H;
   g.M = I;
   g.groups = w->groups;
   g.offsets = offsets;
-  g.n_mblk = (I + 255) / 256;
   g.tiled = w->tiled;
   g.gu = static_cast<__nv_bfloat16*>(const_cast<void*>(gu));   // read only
   g.row_w = row_w;
@@ -887,21 +915,20 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
   g.partial = partial;
   g.status = dev_status;
   g.wait_ns = wait_limit();
-  if ((s = check_launch(launch_train_gemm(TRAIN_HIDDEN, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
+  if ((s = check_launch(launch_train_gemm(TRAIN_HIDDEN, 1, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
   if (d_row_w) {
     s = check_launch(launch_row_w_grad(rows, I / 32, partial, offsets, w->groups, d_row_w, st));
     if (s != MOE_OK) return s;
   }
   if (d_a) {                                           // d_a = d_gu w13
-    s = w->tiled ? make_tmap(&tmA, w->w13, false, 64, static_cast<uint64_t>(w->groups) * 2 * I * (H / 64), 64)
-                 : make_tmap(&tmA, w->w13, false, H, static_cast<uint64_t>(w->groups) * 2 * I, 64);
+    const int subs = train_subs(TRAIN_ROWS, 2 * I);
+    s = make_train_weight_tmap(&tmA, w->w13, TRAIN_ROWS, w->tiled, w->groups, 2 * I, H, subs);
     if (s != MOE_OK) return s;
-    if ((s = make_token_tmaps(&tmB, d_gu, false, 2 * static_cast<uint64_t>(I), rows)) != MOE_OK) return s;
+    if ((s = make_half_tmaps(&tmB, d_gu, 2 * static_cast<uint64_t>(I), rows)) != MOE_OK) return s;
     g.K = 2 * I;
     g.M = H;
-    g.n_mblk = H / 256;
     g.out = static_cast<__nv_bfloat16*>(d_a);
-    if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
+    if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, subs, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
   }
   if (d_w13 || d_w2) {
     WgradArgs q{};
@@ -954,19 +981,19 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
   cudaStream_t st = as_stream(stream);
   if (dx) {                                            // dx = dx_in + d_logits gate
     CUtensorMap tmA;
-    TokenMaps tmB;
-    if ((s = make_tmap(&tmA, gate_w, false, H, E, 64)) != MOE_OK) return s;
-    if ((s = make_token_tmaps(&tmB, d_logits_bf16, false, E, T)) != MOE_OK) return s;
+    HalfMaps tmB;
+    const int subs = train_subs(TRAIN_ROWS, E);
+    if ((s = make_train_weight_tmap(&tmA, gate_w, TRAIN_ROWS, 0, 1, E, H, subs)) != MOE_OK) return s;
+    if ((s = make_half_tmaps(&tmB, d_logits_bf16, E, T)) != MOE_OK) return s;
     TrainGemmArgs g;
     g.rows = T;
     g.K = E;
     g.M = H;
-    g.n_mblk = H / 256;
     g.out = static_cast<__nv_bfloat16*>(dx);
     g.add = static_cast<const __nv_bfloat16*>(dx_in);
     g.status = dev_status;
     g.wait_ns = wait_limit();
-    if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
+    if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, subs, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
   }
   if (d_gate) {                                        // d_gate = d_logits^T x
     WgradArgs q{};

@@ -256,7 +256,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   auto sB = [&](int st) { return smem + st * stage_bytes + kMxA; };
   auto sSfa = [&](int st) { return smem + st * stage_bytes + kMxA + bn * 128u; };
   auto sSfb = [&](int st) { return smem + st * stage_bytes + kMxA + bn * 128u + kMxSfa; };
-  const SegProblem sp{a.rows, a.groups, a.offsets, a.n_mblk, a.bn_max, a.status};
+  const SegProblem sp{a.rows, a.groups, a.offsets, a.n_mblk, a.bn_max, 16, a.status};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMxMaxStages; ++i) {
@@ -294,8 +294,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const uint64_t pol_x = policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
+      int g = 0;
       for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x) {
-        const SegTile ti = decode_tile(sched, sp, t);
+        const SegTile ti = decode_tile(sched, sp, t, g);
         const int row0 = ti.g * a.a_rows_per_group + ti.mb * a.mblk_stride;
         const int row1 = row0 + a.sub1_off;
         const uint8_t* sf0 = a.a_scale + static_cast<size_t>(row0 / 128) * k128 * 512;
@@ -327,8 +328,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
+    int g = 0;
     for (int t = blockIdx.x; t < total && ok && !abort_flag; t += gridDim.x) {
-      const SegTile ti = decode_tile(sched, sp, t);
+      const SegTile ti = decode_tile(sched, sp, t, g);
       const int nrb = (ti.N + 127) / 128;
       uint32_t w[2][2][4];
       auto fetch = [&](int kb) {
@@ -345,8 +347,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       };
       fetch(0);
       for (int kb = 0; kb < nk; ++kb) {
-        if (lane == 0) ok = mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag, a.status, a.wait_ns);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        ok = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, &abort_flag, a.status, a.wait_ns);
         if (!ok) break;
         uint8_t* dst = sSfb(stage);
 #pragma unroll
@@ -370,8 +371,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, it = 0;
+      int g = 0;
       for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x, ++it) {
-        const SegTile ti = decode_tile(sched, sp, t);
+        const SegTile ti = decode_tile(sched, sp, t, g);
         const uint32_t id0 = mxf4_idesc(128u, static_cast<uint32_t>(ti.N), 0u);
         const uint32_t id1 = mxf4_idesc(128u, static_cast<uint32_t>(ti.N), 1u);
         const bool wide = ti.N > 128;
@@ -418,10 +420,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     float* ts = tile_s[warp - 4];
     uint32_t it = 0;
+    int g = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
-      const SegTile ti = decode_tile(sched, sp, t);
+      const SegTile ti = decode_tile(sched, sp, t, g);
       const int nchunk = (ti.N + 31) / 32;
-      if (!mbar_wait(&tmem_full, it & 1u, &abort_flag, a.status, a.wait_ns)) break;
+      if (!mbar_wait_warp(&tmem_full, it & 1u, &abort_flag, a.status, a.wait_ns)) break;
       tc_fence_after();
       if (GATE_UP) {
         uint8_t* out = reinterpret_cast<uint8_t*>(a.out);

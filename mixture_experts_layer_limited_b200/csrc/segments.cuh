@@ -28,6 +28,7 @@ struct SegProblem {
   const int32_t* offsets;   // [groups + 1] or nullptr (one segment of all rows)
   int32_t n_mblk;           // feature blocks per group
   int32_t bn_max;           // max rows per tile (multiple of 32, <= 256)
+  int32_t unit;             // tiles are computed in multiples of this many rows (16 or 32)
   int32_t* status;
 };
 
@@ -81,34 +82,38 @@ __device__ __forceinline__ void build_schedule(SegSched& s, const SegProblem& a,
   }
 }
 
+// a / b for 0 <= a, 0 < b: a float quotient where it is exact (a < 2^20: its
+// error is below a quarter). Every role of a CTA decodes every tile, the loads'
+// and the MMAs' threads between two tiles' work: integer divisions there cost a
+// thousand cycles a tile.
+__device__ __forceinline__ int quick_div(int a, int b) {
+  return a < (1 << 20) ? __float2int_rz(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b))) : a / b;
+}
+
 // Tile `local` of a segment of n rows starting at row seg0 (group g).
 __device__ __forceinline__ SegTile decode_in_segment(const SegProblem& a, int g, int seg0, int n, int local) {
   SegTile ti;
   ti.g = g;
-  const int ntb = (n + a.bn_max - 1) / a.bn_max;
-  const int bn = ((((n + ntb - 1) / ntb) + 15) / 16) * 16;
+  const int ntb = quick_div(n + a.bn_max - 1, a.bn_max);
+  const int bn = (quick_div(n + ntb - 1, ntb) + a.unit - 1) & ~(a.unit - 1);
   const int chunk_tiles = kTbChunk * a.n_mblk;
-  const int chunk = local / chunk_tiles;
+  const int chunk = ntb <= kTbChunk ? 0 : quick_div(local, chunk_tiles);
   const int r = local - chunk * chunk_tiles;
   const int c_tb = min(kTbChunk, ntb - chunk * kTbChunk);   // token blocks in this chunk
-  ti.mb = r / c_tb;
+  ti.mb = quick_div(r, c_tb);
   const int tb = chunk * kTbChunk + (r - ti.mb * c_tb);
   ti.ntb = ntb;
   ti.tb = tb;
   ti.row0 = seg0 + tb * bn;
   ti.n_valid = min(bn, n - tb * bn);
-  ti.N = ((ti.n_valid + 15) / 16) * 16;
+  ti.N = (ti.n_valid + a.unit - 1) & ~(a.unit - 1);
   return ti;
 }
 
-__device__ __forceinline__ SegTile decode_tile(const SegSched& s, const SegProblem& a, int t) {
-  int lo = 0, hi = a.groups - 1;   // last g with tile_start[g] <= t
-  while (lo < hi) {
-    int mid = (lo + hi + 1) >> 1;
-    if (s.tile_start[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  return decode_in_segment(a, lo, s.seg_start[lo], s.seg_start[lo + 1] - s.seg_start[lo],
-                           t - s.tile_start[lo]);
+// Tile t; g: the group of the caller's last tile (0 at first; t only grows).
+__device__ __forceinline__ SegTile decode_tile(const SegSched& s, const SegProblem& a, int t, int& g) {
+  while (t >= s.tile_start[g + 1]) ++g;
+  return decode_in_segment(a, g, s.seg_start[g], s.seg_start[g + 1] - s.seg_start[g], t - s.tile_start[g]);
 }
 
 // Token rows of one stage (a multiple of 16, at most 256) are fetched with at
@@ -145,6 +150,15 @@ __device__ __forceinline__ void store_tile(__nv_bfloat16* stage, const float (&v
     }
   }
   __syncwarp();
+}
+
+// mbar_wait for a whole warp: one lane waits, so that all lanes go on, or give
+// up after an abort, together.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status,
+                                               uint64_t limit_ns) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag, status, limit_ns) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
 // SiLU(g) = g * sigmoid(g). Fast division: for g < -88 the exponential

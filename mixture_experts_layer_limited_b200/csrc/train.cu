@@ -42,9 +42,109 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr) {
 }
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
-// The full-precision exponential: d_row_w is an fp32 output, and __expf's
-// error would be the largest in it.
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// ========================================================================
+// CTA pairs
+// ========================================================================
+// Loads of a CTA of a pair into its own shared memory, completing on a barrier
+// of either CTA (`bar`: its address in the cluster).
+//
+// The TMA unit was the bound of these kernels wherever HBM was not: fitted over
+// their variants, a load costs it about 58 cycles and 20.5 more per KB. So every
+// operand comes as one box a block, as large as the tile allows, and results
+// are stored by the epilogue warps themselves.
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                                 int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                                 int32_t y, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+// A 32-bit shared variable of the other CTA.
+__device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
+// The CTA-pair forms of the tcgen05 calls.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once every MMA issued so far by this thread is done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// Arrives on the first CTA's copy of `bar`. What the arrival hands over is
+// shared memory of this SM that the MMAs read in place: a thread that wrote it
+// has made its stores visible to them with fence.proxy.async before, so the
+// arrival itself needs no order beyond this CTA's (a release at cluster scope
+// waits for a memory barrier of the whole GPU: 870 us instead of 790 for the
+// weight gradients of 251 rows on each of 32 experts). The relaxed form is for
+// threads that wrote nothing.
+__device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_first_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
+               : "memory");
+}
+// Arrives on `bar` of this CTA once every MMA issued so far by this thread is done.
+__device__ __forceinline__ void umma_commit_first(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+// After an abort one CTA may have loaded into a stage what the other had not
+// got to: the first CTA completes the phases both should have filled, arms the
+// one only the second started, so that every load has landed before either CTA
+// leaves. loads[i]: blocks a CTA has loaded into stage i on the first CTA's
+// full[i]; load_bytes[i]: its part of the last one (the same in both CTAs where
+// both loaded it). Called by one thread of the first CTA between two cluster
+// barriers.
+template <int STAGES>
+__device__ void pair_drain(uint64_t* full, const uint32_t* loads, const uint32_t* load_bytes, volatile int* abort_flag,
+                           const int* abort_word) {
+  if (!*abort_flag && ld_cluster(abort_word, 1) == 0) return;
+  for (int i = 0; i < STAGES; ++i) {
+    const uint32_t mine = loads[i], theirs = ld_cluster(&loads[i], 1);
+    if (mine > theirs)
+      asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[i])),
+                   "r"(load_bytes[i])
+                   : "memory");
+    else if (theirs > mine)
+      mbar_arrive_expect_tx(&full[i], ld_cluster(&load_bytes[i], 1));
+    const uint32_t n = mine > theirs ? mine : theirs;
+    if (n) mbar_wait_drain(&full[i], (n - 1) & 1u);
+  }
+}
 
 // ========================================================================
 // Products of a segment's rows with a weight
@@ -89,58 +189,99 @@ __device__ __forceinline__ void spread_tile(__nv_bfloat16* stage, const TileRegs
   __syncwarp();
 }
 
-// Warp roles and tiling as the forward's grouped GEMM: 256 weight-side rows
-// (two 128-row sub-tiles: features f.. and f + 128.., or, forward, the gate and
-// up rows of 128 features) x up to 256 token rows per tile, one accumulator
-// pair in TMEM, three 64-K stages, EPIW epilogue warps.
-template <int MODE, int EPIW>
-__global__ void __launch_bounds__(64 + 32 * EPIW, 1)
-train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ TokenMaps tmB, const TrainGemmArgs a) {
-  constexpr int STAGES = 3, KB = 64;
-  constexpr uint32_t A_SUB_BYTES = 2 * kChunkBytes;
-  constexpr uint32_t STAGE_BYTES = 2 * A_SUB_BYTES + 256 * 128;
+// SiLU's sigmoid with the fast exponential and division (relative error about
+// 2^-21, below that of the tensor cores' fp32 sums it multiplies).
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+// A pair of CTAs shares a tile of SUBS * 256 weight-side rows x up to 256 token
+// rows (M = 256 per MMA, N a multiple of 32), 64 of K a block: each CTA loads
+// its SUBS * 128 weight-side rows and half of the token rows, and has the
+// accumulator rows of its own features for all the tile's token rows.
+//   SUBS = 2 (forward, long K): 48 KB loaded per CTA and block for the products
+//     a lone CTA's 256 x 256 tile loads 64 KB for; the accumulators fill TMEM,
+//     and the four stages loaded meanwhile hide the epilogue.
+//   SUBS = 1 (dh0, and d_a-like products of K <= 512): two accumulators, so that
+//     the epilogue, which is long beside so few products, overlaps the next
+//     tile's MMAs.
+// Measured on B200, this kernel's dh0 and d_a products at V3 widths, 256 rows
+// on each of 32 experts, and at V2-Lite's layer: one CTA per tile of 256 x 256
+// with one accumulator 365 / 445 and 374 / 253 us; SUBS = 1 303 / 568 and
+// 233 / 317 us.
+//   forward: sub-tile 0 holds the gate rows of the CTA's 128 features, sub-tile
+//   1 their up rows, so that one thread has both.
+// Warp 0 loads, warp 1 of the first CTA issues the MMAs, eight epilogue warps:
+// warp w reads TMEM lanes 32 (w % 4).. and every second 32-row chunk.
+template <int MODE, int SUBS>
+struct PairCfg {
+  static constexpr int KB = 64;
+  static constexpr int STAGES = SUBS == 2 ? 4 : 6;
+  static constexpr uint32_t SUB_BYTES = 2 * kChunkBytes;
+  static constexpr uint32_t A_BYTES = SUBS * SUB_BYTES;
+  static constexpr uint32_t STAGE_BYTES = A_BYTES + 128 * 128;
+  static constexpr int ACCS = SUBS == 2 ? 1 : 2;
+  static constexpr int FEATS = MODE == TRAIN_FORWARD ? 256 : SUBS * 256;   // features per tile, half of them per CTA
+  static constexpr int EPIW = 8;
+  static constexpr int THREADS = 64 + 32 * EPIW;
+};
+template <int MODE, int SUBS>
+struct PairSmem {
+  using C = PairCfg<MODE, SUBS>;
+  uint8_t stage[C::STAGES][C::STAGE_BYTES];              // 1024-byte aligned
+  __nv_bfloat16 tile[C::EPIW][32 * 32];
+  uint64_t full_bar[C::STAGES], empty_bar[C::STAGES], tmem_full[2], tmem_empty[2], drain_bar;
+  uint32_t tmem_base;
+  uint32_t loads[C::STAGES];                             // blocks loaded into a stage
+  uint32_t load_bytes[C::STAGES];                        // of the last one, this CTA's part
+  int abort_flag;
+  SegSched sched;
+};
+
+template <int MODE, int SUBS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<MODE, SUBS>::THREADS, 1)
+train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ HalfMaps tmB, const TrainGemmArgs a) {
+  static_assert(MODE != TRAIN_FORWARD || SUBS == 2, "forward: gate and up are the two sub-tiles");
+  static_assert(MODE != TRAIN_HIDDEN || SUBS == 1, "dh0: two accumulators");
+  using C = PairCfg<MODE, SUBS>;
+  constexpr int KB = C::KB, STAGES = C::STAGES, EPIW = C::EPIW, ACCS = C::ACCS;
   extern __shared__ __align__(1024) uint8_t dsmem[];
-  __shared__ SegSched sched;
-  __shared__ __align__(16) __nv_bfloat16 stage_out[EPIW][32 * 32];
-  __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
-  __shared__ uint64_t tmem_full, tmem_empty, drain_bar;
-  __shared__ uint32_t tmem_base_s;
-  __shared__ int issued_parity[STAGES];
-  __shared__ volatile int abort_flag;
-
+  PairSmem<MODE, SUBS>& sm = *reinterpret_cast<PairSmem<MODE, SUBS>*>(dsmem);
+  if ((smem_u32(dsmem) & 1023u) != 0) {                            // the swizzled tiles need it (the same in both CTAs)
+    flag_status(a.status, MOE_DEVSTAT_TIMEOUT);
+    return;
+  }
+  uint64_t *full_bar = sm.full_bar, *empty_bar = sm.empty_bar, *tmem_full = sm.tmem_full, *tmem_empty = sm.tmem_empty;
+  volatile int* abort_flag = &sm.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
-  auto sA = [&](int st) { return smem + st * STAGE_BYTES; };
-  auto sB = [&](int st) { return smem + st * STAGE_BYTES + 2 * A_SUB_BYTES; };
-
-  const SegProblem ga{a.rows, a.groups, a.offsets, a.n_mblk, 256, a.status};
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int first = static_cast<int>(cluster_id_x()), stride = static_cast<int>(gridDim.x) / 2;
+  const SegProblem sp{a.rows, a.groups, a.offsets, a.n_mblk, 256, 32, a.status};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full_bar[i], 1);
       mbar_init(&empty_bar[i], 1);
-      issued_parity[i] = -1;
+      sm.loads[i] = sm.load_bytes[i] = 0;
     }
-    mbar_init(&tmem_full, 1);
-    mbar_init(&tmem_empty, 32 * EPIW);
-    mbar_init(&drain_bar, 1);
-    abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tmem_full[i], 1);
+      mbar_init(&tmem_empty[i], 2 * EPIW);                         // one arrival per epilogue warp of both CTAs
+    }
+    mbar_init(&sm.drain_bar, 1);
+    sm.abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
-    for (int i = 0; i < kTokBoxes; ++i) tma_prefetch_desc(&tmB.box[i]);
+    for (int i = 0; i < 8; ++i) tma_prefetch_desc(&tmB.box[i]);
   }
-  if (warp == 1) {
-    tmem_alloc(&tmem_base_s, 512);
-    tmem_relinquish();
-  }
-  if (warp == 2) build_schedule(sched, ga, lane);
+  if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 512);
+  if (warp == 2) build_schedule(sm.sched, sp, lane);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                                                  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
-  const uint32_t tmem_base = tmem_base_s;
-  const int total = sched.tile_start[a.groups];
+  const uint32_t tmem_base = sm.tmem_base;
+  const int total = sm.sched.tile_start[a.groups];
   const int nk = (a.K + KB - 1) / KB;
 
   if (warp == 0) {
@@ -150,183 +291,191 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       const uint64_t pol_x = policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
-      for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x) {
-        const SegTile ti = decode_tile(sched, ga, t);
-        const int m0 = ti.mb * 256;
-        const int nch = MODE == TRAIN_FORWARD ? 4 : min(4, (a.M - m0 + 63) / 64);   // 8 KB pieces of A
+      bool ok = true;
+      int group = 0;
+      for (int t = first; t < total && ok && !*abort_flag; t += stride) {
+        const SegTile ti = decode_tile(sm.sched, sp, t, group);
         const uint64_t pol_w = ti.ntb > 1 ? pol_reuse : pol_once;
-        const uint32_t bytes = static_cast<uint32_t>(nch) * kChunkBytes + static_cast<uint32_t>(ti.N) * 128u;
-        bool ok = true;
+        const uint32_t bytes = C::A_BYTES + static_cast<uint32_t>(ti.N) * 64u;   // this CTA's half of a block
+        const CUtensorMap* mB = &tmB.box[ti.N / 32 - 1];
+        const int brow = ti.row0 + rank * (ti.N / 2);
+        const int m0 = ti.mb * C::FEATS + C::FEATS / 2 * rank;      // this CTA's first feature
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag, a.status, a.wait_ns)) { ok = false; break; }
-          mbar_arrive_expect_tx(&full_bar[stage], bytes);
-          int bx = kb * KB;                                         // this K block in the rows' operand
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, a.status, a.wait_ns)) { ok = false; break; }
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);
+          ++sm.loads[stage];
+          sm.load_bytes[stage] = bytes;
+          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+          // the weight's box of this block (make_train_weight_tmap), and the block in the rows' operand
+          int x = 0, y = 0, z = 0, bx = kb * KB;
           if (MODE == TRAIN_FORWARD) {
-            if (a.tiled) {                                          // gate rows, then up rows: one block
-              tma_load_2d(sA(stage), &tmA, &full_bar[stage], 0, ((ti.g * a.n_mblk + ti.mb) * nk + kb) * 256, pol_w);
+            if (a.tiled) {
+              z = (ti.g * (a.M / 128) + m0 / 128) * nk + kb;
             } else {
-              const int y = ti.g * 2 * a.M + ti.mb * 128;
-              tma_load_2d(sA(stage), &tmA, &full_bar[stage], kb * KB, y, pol_w);
-              tma_load_2d(sA(stage) + A_SUB_BYTES, &tmA, &full_bar[stage], kb * KB, y + a.M, pol_w);
+              x = kb * KB;
+              y = m0;
+              z = 2 * ti.g;
             }
+          } else if (a.tiled) {
+            y = (kb & 3) * 64;
+            z = (ti.g * (a.K / 256) + (kb >> 2)) * (a.M / 64) + m0 / 64;
+            if (MODE == TRAIN_ROWS)                                 // K runs in the tiled w13's row order
+              bx = (kb >> 2) * 128 + (kb & 1) * 64 + ((kb & 2) ? a.K / 2 : 0);
           } else {
-            if (MODE == TRAIN_ROWS && a.tiled) {                    // K runs in the tiled w13's row order
-              const int sub = kb & 3;
-              bx = (kb >> 2) * 128 + (sub & 1) * 64 + (sub >= 2 ? a.K / 2 : 0);
-            }
-            for (int j = 0; j < nch; ++j) {
-              int x = m0 + 64 * j, y = ti.g * a.K + kb * KB;
-              if (a.tiled) {                                        // the block of 256 K rows x 64 features, its rows of kb
-                y = ((ti.g * (a.K / 256) + (kb >> 2)) * (a.M / 64) + x / 64) * 256 + (kb & 3) * 64;
-                x = 0;
-              }
-              tma_load_2d(sA(stage) + j * kChunkBytes, &tmA, &full_bar[stage], x, y, pol_w);
-            }
+            y = ti.g * a.K + kb * KB;
+            z = m0 / 64;
           }
-          uint8_t* bdst = sB(stage);
-          uint64_t* fb = &full_bar[stage];
-          load_token_rows(ti.N, [&](int which, int off) {
-            tma_load_2d(bdst + off * 128, &tmB.box[which], fb, bx, ti.row0 + off, pol_x);
-          });
-          issued_parity[stage] = static_cast<int>(phase);
+          tma_load_3d_pair(sm.stage[stage], &tmA, bar, x, y, z, pol_w);
+          tma_load_2d_pair(sm.stage[stage] + C::A_BYTES, mB, bar, bx, brow, pol_x);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (!ok) break;
-      }
-      if (abort_flag) {   // let every issued copy land before the CTA exits
-        for (int i = 0; i < STAGES; ++i)
-          if (issued_parity[i] >= 0) mbar_wait_drain(&full_bar[i], static_cast<uint32_t>(issued_parity[i]));
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, it = 0;
-      for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x, ++it) {
-        const SegTile ti = decode_tile(sched, ga, t);
-        const bool two = MODE == TRAIN_FORWARD || a.M - ti.mb * 256 > 128;
-        const uint32_t idesc = make_idesc(1u, 128u, static_cast<uint32_t>(ti.N)) | (MODE == TRAIN_FORWARD ? 0u : kIdescAMn);
-        if (!mbar_wait(&tmem_empty, (it & 1u) ^ 1u, &abort_flag, a.status, a.wait_ns)) break;
+    if (rank == 0 && lane == 0) {
+      // as little as possible between the blocks' MMAs (see wgrad_kernel)
+      constexpr uint64_t kA = MODE == TRAIN_FORWARD ? 2 : 128, kB = 2;   // descriptor units (16 B) per K step of 16
+      const uint64_t ad0 = MODE == TRAIN_FORWARD ? sw128_desc(smem_u32(sm.stage[0])) : mn_desc(smem_u32(sm.stage[0]));
+      const uint64_t bd0 = sw128_desc(smem_u32(sm.stage[0]) + C::A_BYTES);
+      int st = 0;
+      uint32_t it = 0, phase = 0;
+      bool ok = true;
+      int group = 0;
+      for (int t = first; t < total && ok; t += stride, ++it) {
+        const SegTile ti = decode_tile(sm.sched, sp, t, group);
+        const uint32_t idesc = make_idesc(1u, 256u, static_cast<uint32_t>(ti.N)) | (MODE == TRAIN_FORWARD ? 0u : kIdescAMn);
+        const uint32_t ac = it % ACCS, ac_ph = (it / ACCS) & 1u;
+        const uint32_t d0 = tmem_base + ac * 256;
+        ok = mbar_wait(&tmem_empty[ac], ac_ph ^ 1u, abort_flag, a.status, a.wait_ns);
+        if (!ok) break;
         tc_fence_after();
-        bool ok = true;
+        uint32_t acc = 0;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&full_bar[stage], phase, &abort_flag, a.status, a.wait_ns)) { ok = false; break; }
+          ok = mbar_wait(&full_bar[st], phase, abort_flag, a.status, a.wait_ns);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA(stage)), b0 = smem_u32(sB(stage));
+          const uint64_t ad = ad0 + st * (C::STAGE_BYTES >> 4), bd = bd0 + st * (C::STAGE_BYTES >> 4);
 #pragma unroll
           for (int kk = 0; kk < KB / 16; ++kk) {
-            const uint32_t acc = (kb | kk) != 0;
-            const uint64_t bd = sw128_desc(b0 + kk * 32);
-            const uint64_t ad = MODE == TRAIN_FORWARD ? sw128_desc(a0 + kk * 32) : mn_desc(a0 + kk * 2048);
-            const uint64_t ad1 = MODE == TRAIN_FORWARD ? sw128_desc(a0 + A_SUB_BYTES + kk * 32)
-                                                       : mn_desc(a0 + A_SUB_BYTES + kk * 2048);
-            umma_bf16(tmem_base, ad, bd, idesc, acc);
-            if (two) umma_bf16(tmem_base + 256, ad1, bd, idesc, acc);
+#pragma unroll
+            for (int s = 0; s < SUBS; ++s)
+              umma_bf16_pair(d0 + s * 256, ad + s * (C::SUB_BYTES >> 4) + kk * kA, bd + kk * kB, idesc, acc);
+            acc = 1;
           }
-          umma_commit(&empty_bar[stage]);
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          umma_commit_pair(&empty_bar[st]);
+          if (++st == STAGES) { st = 0; phase ^= 1u; }
         }
-        if (!ok) break;
-        umma_commit(&tmem_full);
+        if (ok) umma_commit_pair(&tmem_full[ac]);
       }
-      umma_commit(&drain_bar);   // all issued MMAs must finish before TMEM is released
-      mbar_wait_drain(&drain_bar, 0);
+      umma_commit_first(&sm.drain_bar);                            // all issued MMAs must finish before TMEM is released
+      mbar_wait_drain(&sm.drain_bar, 0);
     }
   } else {
-    const int q = warp & 3;
+    const int q = warp & 3, c0 = (warp - 2) / 4;
     constexpr int cstep = EPIW / 4;
-    const int c0 = (warp - 2) / 4;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-    __nv_bfloat16* stg = stage_out[warp - 2];
+    const size_t ld = 2 * static_cast<size_t>(a.M);                // of the pre-activations and their gradients
+    __nv_bfloat16* stg = sm.tile[warp - 2];
     uint32_t it = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
-      const SegTile ti = decode_tile(sched, ga, t);
+    int group = 0;
+    for (int t = first; t < total; t += stride, ++it) {
+      const SegTile ti = decode_tile(sm.sched, sp, t, group);
       const int nchunk = (ti.N + 31) / 32;
-      const int nsub = MODE != TRAIN_FORWARD && a.M - ti.mb * 256 > 128 ? 2 : 1;
-      // this warp's pieces of 32 features x 32 rows: sub-tile s (forward: both at once), chunk c
-      const int per = c0 < nchunk ? (nchunk - c0 + cstep - 1) / cstep : 0;
-      const int pieces = nsub * per;
+      const uint32_t ac = it % ACCS, ac_ph = (it / ACCS) & 1u;
+      const uint32_t acc0 = lane_addr + ac * 256;
+      const int f0 = ti.mb * C::FEATS + C::FEATS / 2 * rank + 32 * q;
+      constexpr int PASSES = MODE == TRAIN_FORWARD ? 1 : SUBS;     // sub-tiles of features
+      // the first piece's other inputs, before the wait
       TileRegs gr, ur;
-      if (MODE == TRAIN_HIDDEN && pieces > 0) {                                   // the first piece's pre-activations, before the wait
-        const int f = ti.mb * 256 + 32 * q, r = c0 * 32;
-        gr = load_tile_regs(a.gu, 2 * static_cast<size_t>(a.M), ti.row0 + r, ti.n_valid - r, f, lane);
-        ur = load_tile_regs(a.gu, 2 * static_cast<size_t>(a.M), ti.row0 + r, ti.n_valid - r, a.M + f, lane);
+      const bool mine = f0 < a.M && c0 < nchunk;                   // the last tile of a matrix may be part empty
+      if (MODE == TRAIN_HIDDEN && mine) {
+        gr = load_tile_regs(a.gu, ld, ti.row0 + c0 * 32, ti.n_valid - c0 * 32, f0, lane);
+        ur = load_tile_regs(a.gu, ld, ti.row0 + c0 * 32, ti.n_valid - c0 * 32, a.M + f0, lane);
       }
-      if (!mbar_wait(&tmem_full, it & 1u, &abort_flag, a.status, a.wait_ns)) break;
+      if (MODE == TRAIN_ROWS && mine && a.add)
+        gr = load_tile_regs(a.add, static_cast<size_t>(a.M), ti.row0 + c0 * 32, ti.n_valid - c0 * 32, f0, lane);
+      if (!mbar_wait_warp(&tmem_full[ac], ac_ph, abort_flag, a.status, a.wait_ns)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int p = 0; p < pieces; ++p) {
-        const int s = p / per, c = c0 + (p - s * per) * cstep;
-        const int feat0 = MODE == TRAIN_FORWARD ? ti.mb * 128 + 32 * q : ti.mb * 256 + s * 128 + 32 * q;
-        const int row0 = ti.row0 + c * 32, n_rows = ti.n_valid - c * 32;
-        float v[32];
-        tmem_ld32(lane_addr + s * 256 + c * 32, v);
-        if (MODE == TRAIN_FORWARD) {
-          // h from the fp32 sums; the pre-activations are rounded once, for the backward pass
-          float u[32];
-          tmem_ld32(lane_addr + 256 + c * 32, u);
-          tmem_ld_wait();
-          const size_t ld = 2 * static_cast<size_t>(a.M);
-          store_tile<32>(stg, v, lane, a.gu, ld, row0, n_rows, feat0);
-          store_tile<32>(stg, u, lane, a.gu, ld, row0, n_rows, a.M + feat0);
+      for (int s = 0; s < PASSES; ++s) {
+        const int feat0 = f0 + s * 128;
+        if (feat0 >= a.M) break;
+        const uint32_t acc = acc0 + s * 256;
+#pragma unroll 1
+        for (int c = c0; c < nchunk; c += cstep) {
+          const int row0 = ti.row0 + c * 32, n_rows = ti.n_valid - c * 32;
+          const int row1 = row0 + 32 * cstep, n_rows1 = n_rows - 32 * cstep;   // the next chunk's
+          float v[32];
+          tmem_ld32(acc + c * 32, v);
+          if (MODE == TRAIN_FORWARD) {
+            // h from the fp32 sums; the pre-activations are rounded once, for the backward pass
+            float u[32];
+            tmem_ld32(acc + 256 + c * 32, u);
+            tmem_ld_wait();
+            store_tile<32>(stg, v, lane, a.gu, ld, row0, n_rows, feat0);
+            store_tile<32>(stg, u, lane, a.gu, ld, row0, n_rows, a.M + feat0);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = silu(v[j]) * u[j];
-          store_tile<32>(stg, v, lane, a.h, static_cast<size_t>(a.M), row0, n_rows, feat0);
-          continue;
-        }
-        tmem_ld_wait();
-        if (MODE == TRAIN_HIDDEN) {
-          const size_t ld = 2 * static_cast<size_t>(a.M);
-          const float w = (lane < n_rows) ? (a.row_w ? __ldg(a.row_w + row0 + lane) : 1.0f) : 0.0f;
-          float g[32], u[32];
-          spread_tile(stg, gr, lane, g);
-          spread_tile(stg, ur, lane, u);
-          if (p + 1 < pieces) {                                     // the next piece's, while this one is computed
-            const int s2 = (p + 1) / per, c2 = c0 + (p + 1 - s2 * per) * cstep;
-            const int f2 = ti.mb * 256 + s2 * 128 + 32 * q;
-            gr = load_tile_regs(a.gu, ld, ti.row0 + c2 * 32, ti.n_valid - c2 * 32, f2, lane);
-            ur = load_tile_regs(a.gu, ld, ti.row0 + c2 * 32, ti.n_valid - c2 * 32, a.M + f2, lane);
-          }
-          // g <- dg, u <- du, v <- h dh0 / row_w * h: one value at a time
-          float hw[32];
+            for (int j = 0; j < 32; ++j) v[j] = silu(v[j]) * u[j];
+            store_tile<32>(stg, v, lane, a.h, static_cast<size_t>(a.M), row0, n_rows, feat0);
+          } else if (MODE == TRAIN_HIDDEN) {
+            tmem_ld_wait();
+            const float w = lane < n_rows ? (a.row_w ? __ldg(a.row_w + row0 + lane) : 1.0f) : 0.0f;
+            float g[32], u[32], hw[32];
+            spread_tile(stg, gr, lane, g);
+            spread_tile(stg, ur, lane, u);
+            if (c + cstep < nchunk) {                              // the next chunk's, while this one is computed
+              gr = load_tile_regs(a.gu, ld, row1, n_rows1, feat0, lane);
+              ur = load_tile_regs(a.gu, ld, row1, n_rows1, a.M + feat0, lane);
+            }
+            // g <- dg, u <- du, v <- h dh0, hw = row_w h
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, j);
-            const float sg = sigmoid(g[j]);
-            const float act = g[j] * sg;                            // SiLU(g)
-            const float dh = v[j] * wj;
-            const float h = act * u[j];
-            v[j] *= h;
-            hw[j] = h * wj;
-            const float dg = dh * u[j] * sg * fmaf(g[j], 1.0f - sg, 1.0f);
-            u[j] = dh * act;
-            g[j] = dg;
-          }
-          store_tile<32>(stg, g, lane, a.d_gu, ld, row0, n_rows, feat0);
-          store_tile<32>(stg, u, lane, a.d_gu, ld, row0, n_rows, a.M + feat0);
-          store_tile<32>(stg, hw, lane, a.h, static_cast<size_t>(a.M), row0, n_rows, feat0);
-          const float part = lane_sums(v, lane);
-          if (lane < n_rows) a.partial[static_cast<size_t>(feat0 / 32) * a.rows + row0 + lane] = part;
-        } else {
-          if (a.add) {
-            float add[32];
-            const TileRegs ar = load_tile_regs(a.add, static_cast<size_t>(a.M), row0, n_rows, feat0, lane);
-            spread_tile(stg, ar, lane, add);
+            for (int j = 0; j < 32; ++j) {
+              const float wj = __shfl_sync(0xffffffffu, w, j);
+              const float sg = sigmoid(g[j]);
+              const float act = g[j] * sg;                         // SiLU(g)
+              const float dh = v[j] * wj;
+              const float h = act * u[j];
+              v[j] *= h;
+              hw[j] = h * wj;
+              const float dg = dh * u[j] * sg * fmaf(g[j], 1.0f - sg, 1.0f);
+              u[j] = dh * act;
+              g[j] = dg;
+            }
+            store_tile<32>(stg, g, lane, a.d_gu, ld, row0, n_rows, feat0);
+            store_tile<32>(stg, u, lane, a.d_gu, ld, row0, n_rows, a.M + feat0);
+            store_tile<32>(stg, hw, lane, a.h, static_cast<size_t>(a.M), row0, n_rows, feat0);
+            const float part = lane_sums(v, lane);
+            if (lane < n_rows) a.partial[static_cast<size_t>(feat0 / 32) * a.rows + row0 + lane] = part;
+          } else {
+            tmem_ld_wait();
+            if (a.add) {
+              float add[32];
+              spread_tile(stg, gr, lane, add);
+              if (c + cstep < nchunk)
+                gr = load_tile_regs(a.add, static_cast<size_t>(a.M), row1, n_rows1, feat0, lane);
+              else if (s + 1 < PASSES && feat0 + 128 < a.M)
+                gr = load_tile_regs(a.add, static_cast<size_t>(a.M), ti.row0 + c0 * 32, ti.n_valid - c0 * 32, feat0 + 128,
+                                    lane);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += add[j];
+              for (int j = 0; j < 32; ++j) v[j] += add[j];
+            }
+            store_tile<32>(stg, v, lane, a.out, static_cast<size_t>(a.M), row0, n_rows, feat0);
           }
-          store_tile<32>(stg, v, lane, a.out, static_cast<size_t>(a.M), row0, n_rows, feat0);
         }
       }
       tc_fence_before();
-      mbar_arrive(&tmem_empty);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[ac]);
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                                                  // neither CTA issues anything any more
+  if (rank == 0 && threadIdx.x == 0) pair_drain<STAGES>(sm.full_bar, sm.loads, sm.load_bytes, abort_flag, &sm.abort_flag);
+  cluster_sync();                                                  // nothing of either CTA is used any more
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, 512);
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
 }
 
 // d_row_w[r] = sum of the row's partial sums, in feature order; rows outside
@@ -348,24 +497,27 @@ row_w_grad_kernel(int rows, int n, const float* __restrict__ partial, const int3
 // A pair of CTAs (a cluster of two) shares one tile of 256 features of A by 256
 // of B (128 where N leaves no more), K = the segment's rows in blocks of 64:
 // tcgen05.mma.cta_group::2 with M = 256. Each CTA holds 128 features of A and
-// half of B's in shared memory and the accumulator rows of its 128 features in
-// TMEM. A CTA so loads 32 KB per block for the products a lone CTA would load
-// 48 KB for, and the accumulator takes 256 of the 512 TMEM columns: two of them,
-// so a tile's epilogue overlaps the next tile's products. Both count: where a
-// segment has few rows the output's bytes bound the work, else the operands'
-// way from L2 does. Measured on B200 (V3 widths, 32 experts): one CTA per tile
-// of 128 x 256 with two accumulators 933 us at 256 rows per expert and 2815 us
-// at 1024; 256 x 256 with one accumulator 935 and 2523 us.
+// half of B's in shared memory and the accumulator rows of its features in TMEM,
+// twice (2 x 256 columns), so that a tile's stores overlap the next tile's
+// products. Long segments are bound by the tensor cores under the power cap,
+// segments of a few rows by the output's bytes.
 //
-// Warp 0 loads its CTA's operands (64 rows x 128 features a load); both CTAs'
-// loads complete on the first CTA's full_bar, whose warp 1 issues the MMAs for
-// both and commits to both. A last block with rows behind the segment's end in
-// its last step goes another way: each CTA's loads complete on a barrier of its
-// own, its last warp zeroes those rows and arrives on the first CTA's
-// tail_done. (With such a handshake for every block, or the zeroing on the MMA
-// warp, its latency set the pace: 251 rows per expert cost 1.5 times what 256
-// do.) Eight warps take the accumulator to shared memory as 128-byte-swizzled
-// boxes and store them with TMA (bf16, or fp32 added to what is there).
+// Warp 0 loads its CTA's operands (one box each a block); both CTAs' loads
+// complete on the first CTA's full_bar, whose warp 1 issues the MMAs for both
+// and commits to both. Eight warps take the accumulator to shared memory as
+// 128-byte-swizzled boxes of 32 rows and store them with TMA (bf16, or fp32,
+// stored or added to what is there). Rows behind the segment's end in its last K
+// step are zeroed in both operands by a warp of their own (a neighbour's row may
+// hold anything, and 0 * NaN is NaN); that block's loads complete on a barrier of
+// each CTA's own.
+//
+// Measured on B200 at V3 widths, 32 experts: 256 rows each 777 us (3.6 TB/s
+// written, 930 TFLOP/s), 251 rows 792 us, 16 rows 470 us (6.0 TB/s written).
+// What was slower at 256 rows: one CTA per tile of 256 x 256 with one
+// accumulator 935 us; the warps storing 16 or 32 bytes a thread themselves 890
+// and 970; 128-row store boxes 808; B's blocks kept for a run of eight tiles,
+// two fifths of the loads saved, 790: neither loads nor stores alone set the
+// pace, and with operands of zeros, which draw less power, 672 us are left.
 struct WgradCfg {
   static constexpr int KB = 64;                          // rows per stage
   static constexpr int STAGES = 6;
@@ -379,92 +531,57 @@ struct WgradCfg {
 struct WgradSmem {
   using C = WgradCfg;
   uint8_t stage[C::STAGES][C::STAGE_BYTES];              // 1024-byte aligned
-  uint8_t out[C::EPIW][32 * 128];
+  uint8_t out[C::EPIW][32 * 128];                        // one store box per epilogue warp
   uint64_t full_bar[C::STAGES], tail_full[C::STAGES], tail_done[C::STAGES], empty_bar[C::STAGES];
   uint64_t tmem_full[2], tmem_empty[2], drain_bar;
   uint32_t tmem_base;
-  uint32_t loads[C::STAGES], tails[C::STAGES];           // loads issued into a stage, on full_bar and on tail_full
+  uint32_t loads[C::STAGES], tails[C::STAGES];           // blocks loaded into a stage, on full_bar and on tail_full
+  uint32_t load_bytes[C::STAGES];
   int abort_flag;
   int off[kMaxGroups + 1];
 };
 
-// Loads of a CTA of a pair into its own shared memory, completing on a barrier
-// of either CTA (`bar`: its address in the cluster). 3-D: one box of a matrix
-// seen as [N / 64] column blocks of [rows, 64]: 64 rows of two column blocks,
-// each block's rows contiguous in shared memory.
-__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t row,
-                                                 int32_t block, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row), "r"(block), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t x,
-                                                 int32_t y, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
-      : "memory");
-}
-// A 32-bit shared variable of the other CTA.
-__device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
-  return v;
-}
-
-// The CTA-pair forms of the tcgen05 calls.
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrives on `bar` of both CTAs once every MMA issued so far by this thread is done.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-// Arrives on the first CTA's copy of `bar` (release at cluster scope); relaxed
-// where the thread has written nothing that is read after the barrier.
-__device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_first_relaxed(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
-               : "memory");
-}
-
-struct WgradTile { int p, g, m, n, k0, kn; };
+// The tiles of a pair, `stride` apart, in order: problem p, group g, blocks mi
+// and ni (fastest) of 256 features of A and B. Steps by adding with carries:
+// divisions a tile cost its MMAs a third of their time at 256 rows.
+struct WgradIter {
+  int t, stride, p, g, mi, ni;
+  int step_g, step_m, step_n;                            // stride in this problem's groups, mi and ni
+  __device__ __forceinline__ void place(const WgradArgs& a) {
+    const bool second = t >= a.prob[0].tiles;
+    p = second ? 1 : 0;
+    const int local = second ? t - a.prob[0].tiles : t;
+    const int per = a.prob[p].per_group, nn = a.prob[p].n_blocks;
+    g = local / per;
+    mi = (local - g * per) / nn;
+    ni = local - g * per - mi * nn;
+    step_g = stride / per;
+    step_m = (stride - step_g * per) / nn;
+    step_n = stride - step_g * per - step_m * nn;
+  }
+  __device__ __forceinline__ WgradIter(const WgradArgs& a, int first, int stride_) : t(first), stride(stride_) { place(a); }
+  __device__ __forceinline__ void next(const WgradArgs& a, int total) {
+    t += stride;
+    if (t >= total) return;
+    if (p == 0 && t >= a.prob[0].tiles) { place(a); return; }
+    const int nn = a.prob[p].n_blocks, nm = a.prob[p].m_blocks;
+    ni += step_n;
+    mi += step_m;
+    g += step_g;
+    if (ni >= nn) { ni -= nn; ++mi; }
+    if (mi >= nm) { mi -= nm; ++g; }
+  }
+};
+struct WgradTile { int p, g, m, n, N, k0, kn; };
 
 // `off`: the segments' starts in shared memory, cut to the rows there are.
-__device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* off, int t) {
+__device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* off, const WgradIter& i) {
   WgradTile w;
-  w.p = a.n_prob > 1 && t >= a.prob[0].tiles ? 1 : 0;
-  if (w.p) t -= a.prob[0].tiles;
-  const WgradProblem& pr = a.prob[w.p];
-  w.g = t / pr.per_group;
-  const int r = t - w.g * pr.per_group;
-  const int mi = r / pr.n_blocks;
-  w.m = mi * 256;
-  w.n = (r - mi * pr.n_blocks) * 256;
+  w.p = i.p;
+  w.g = i.g;
+  w.m = i.mi * 256;
+  w.n = i.ni * 256;
+  w.N = a.prob[i.p].N;
   w.k0 = off[w.g];
   w.kn = off[w.g + 1] - w.k0;
   return w;
@@ -499,6 +616,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       mbar_init(&sm.tail_done[i], 2);                            // both CTAs' tail warps
       mbar_init(&empty_bar[i], 1);
       sm.loads[i] = sm.tails[i] = 0;
+      sm.load_bytes[i] = C::STAGE_BYTES;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tmem_full[i], 1);
@@ -529,11 +647,11 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; t < total && ok && !*abort_flag; t += stride) {
-        const WgradTile w = wgrad_tile(a, off, t);
+      for (WgradIter i(a, first, stride); i.t < total && ok && !*abort_flag; i.next(a, total)) {
+        const WgradTile w = wgrad_tile(a, off, i);
         const WgradProblem& pr = a.prob[w.p];
         const int m = w.m + 128 * rank;
-        const int nb = w.n / 64 + (pr.N - w.n > 128 ? 2 : 1) * rank;    // this CTA's half of B's features
+        const int nb = w.n / 64 + (w.N - w.n > 128 ? 2 : 1) * rank;    // this CTA's half of B's features
         for (int k = 0; k < w.kn; k += KB) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, a.status, a.wait_ns)) { ok = false; break; }
           const bool tail = w.kn - k <= KB && (w.kn & 15);         // rows to zero
@@ -551,9 +669,9 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
             tma_load_2d_pair(sA(stage), &pr.tmA, bar, m, w.k0 + k, pol);
             tma_load_2d_pair(sA(stage) + kChunkBytes, &pr.tmA, bar, m + 64, w.k0 + k, pol);
           } else {
-            tma_load_3d_pair(sA(stage), &pr.tmA, bar, w.k0 + k, m / 64, pol);
+            tma_load_3d_pair(sA(stage), &pr.tmA, bar, 0, w.k0 + k, m / 64, pol);
           }
-          tma_load_3d_pair(sB(stage), &pr.tmB, bar, w.k0 + k, nb, pol);
+          tma_load_3d_pair(sB(stage), &pr.tmB, bar, 0, w.k0 + k, nb, pol);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
@@ -570,9 +688,9 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       int st = 0;
       uint32_t it = 0, full_par = 0, tail_par = 0;                 // parity of each stage's next wait, by barrier
       bool ok = true;
-      for (int t = first; t < total && ok; t += stride, ++it) {
-        const WgradTile w = wgrad_tile(a, off, t);
-        const uint32_t idesc = make_idesc(1u, 256u, a.prob[w.p].N - w.n > 128 ? 256u : 128u) | kIdescAMn | kIdescBMn;
+      for (WgradIter i(a, first, stride); i.t < total && ok; i.next(a, total), ++it) {
+        const WgradTile w = wgrad_tile(a, off, i);
+        const uint32_t idesc = make_idesc(1u, 256u, w.N - w.n > 128 ? 256u : 128u) | kIdescAMn | kIdescBMn;
         const uint32_t d0 = tmem_base + (it & 1u) * 256;
         const int even = w.kn / KB, rest = w.kn - even * KB;       // blocks of 64 rows, and the last one's rows
         ok = mbar_wait(&tmem_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, abort_flag, a.status, a.wait_ns);
@@ -614,24 +732,20 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
         if (ok) umma_commit_pair(&tmem_full[it & 1u]);
       }
       // all issued MMAs must finish before TMEM is released
-      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                       smem_u32(&sm.drain_bar))
-                   : "memory");
+      umma_commit_first(&sm.drain_bar);
       mbar_wait_drain(&sm.drain_bar, 0);
     }
   } else if (warp == 2 + EPIW) {
     // rows behind the segment's end in the last block: zeroed as soon as they land
     int stage = 0;
     uint32_t par = 0;
-    for (int t = first; t < total; t += stride) {
-      const WgradTile w = wgrad_tile(a, off, t);
+    for (WgradIter i(a, first, stride); i.t < total; i.next(a, total)) {
+      const WgradTile w = wgrad_tile(a, off, i);
       const int blocks = (max(w.kn, 0) + KB - 1) / KB;
       if (w.kn & 15) {
         const int st = (stage + blocks - 1) % STAGES;
         const int valid = w.kn - (blocks - 1) * KB;
-        bool ok = true;
-        if (lane == 0) ok = mbar_wait(&sm.tail_full[st], (par >> st) & 1u, abort_flag, a.status, a.wait_ns);
-        if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0) == 0) break;
+        if (!mbar_wait_warp(&sm.tail_full[st], (par >> st) & 1u, abort_flag, a.status, a.wait_ns)) break;
         par ^= 1u << st;
         const int nz = ((valid + 15) / 16 * 16 - valid) * 128;     // bytes per box: A's two boxes, then B's
         uint8_t* base = sA(st) + valid * 128;
@@ -647,20 +761,21 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
   } else {
     const int q = warp & 3, half = (warp - 2) / 4;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-    uint8_t* box = sm.out[warp - 2];
-    const int cols = a.f32 ? 32 : 64;                              // columns of a 128-byte box row
+    uint8_t* box = sm.out[warp - 2];                               // 32 rows x 128 B
+    const int cols = a.f32 ? 32 : 64;                              // columns of such a row
     uint32_t it = 0;
-    for (int t = first; t < total; t += stride, ++it) {
-      const WgradTile w = wgrad_tile(a, off, t);
+    for (WgradIter i(a, first, stride); i.t < total; i.next(a, total), ++it) {
+      const WgradTile w = wgrad_tile(a, off, i);
       const WgradProblem& pr = a.prob[w.p];
-      const int width = pr.N - w.n > 128 ? 256 : 128;
+      const int width = w.N - w.n > 128 ? 256 : 128;
       const int m = w.m + 128 * rank + 32 * q;                     // this warp's 32 features of A
       const uint32_t acc = lane_addr + (it & 1u) * 256;
-      if (!mbar_wait(&tmem_full[it & 1u], (it >> 1) & 1u, abort_flag, a.status, a.wait_ns)) break;
+      if (!mbar_wait_warp(&tmem_full[it & 1u], (it >> 1) & 1u, abort_flag, a.status, a.wait_ns)) break;
       tc_fence_after();
       const bool empty = w.kn <= 0;
       // adding nothing needs no store, and rows past the matrix have none
       if (!(empty && a.accumulate) && m < pr.M) {
+#pragma unroll 1
         for (int c = half * cols; c < width; c += 2 * cols) {
           float v[32], v2[32];
           if (!empty) {
@@ -717,22 +832,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                                  // neither CTA issues anything any more
-  // After an abort one CTA may have loaded into a stage what the other had not
-  // got to: complete the phases both started, arm the one only the second
-  // started, so that every load has landed before either CTA leaves.
-  if (rank == 0 && threadIdx.x == 0 && (*abort_flag || ld_cluster(&sm.abort_flag, 1) != 0)) {
-    for (int i = 0; i < STAGES; ++i) {
-      const uint32_t mine = sm.loads[i], theirs = ld_cluster(&sm.loads[i], 1);
-      if (mine > theirs)
-        asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full_bar[i])),
-                     "r"(C::STAGE_BYTES)
-                     : "memory");
-      else if (theirs > mine)
-        mbar_arrive_expect_tx(&full_bar[i], C::STAGE_BYTES);
-      const uint32_t n = mine > theirs ? mine : theirs;
-      if (n) mbar_wait_drain(&full_bar[i], (n - 1) & 1u);
-    }
-  }
+  if (rank == 0 && threadIdx.x == 0) pair_drain<STAGES>(sm.full_bar, sm.loads, sm.load_bytes, abort_flag, &sm.abort_flag);
   cluster_sync();                                                  // nothing of either CTA is used any more
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
@@ -831,16 +931,28 @@ route_backward_kernel(int T, int E, int k, int scoring, int norm, float scale, c
 // ------------------------------------------------------------------------
 // host-side launch helpers (called from api.cu)
 // ------------------------------------------------------------------------
-cudaError_t launch_train_gemm(int mode, const CUtensorMap& tmA, const TokenMaps& tmB, const TrainGemmArgs& a, int grid,
+template <int MODE, int SUBS>
+static cudaError_t train_gemm(const CUtensorMap& tmA, const HalfMaps& tmB, TrainGemmArgs a, int num_sms,
                               cudaStream_t stream) {
-  const size_t smem = 3 * (4 * kChunkBytes + 256 * 128) + 1024;
-  constexpr int W = 8;
-  auto kern = mode == TRAIN_FORWARD ? train_gemm_kernel<TRAIN_FORWARD, W>
-              : mode == TRAIN_HIDDEN ? train_gemm_kernel<TRAIN_HIDDEN, W> : train_gemm_kernel<TRAIN_ROWS, W>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  using C = PairCfg<MODE, SUBS>;
+  constexpr size_t smem = sizeof(PairSmem<MODE, SUBS>);
+  static_assert(smem <= 232448, "train_gemm_kernel's shared memory exceeds an SM's");
+  cudaError_t e = cudaFuncSetAttribute(train_gemm_kernel<MODE, SUBS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kern<<<grid, 64 + 32 * W, smem, stream>>>(tmA, tmB, a);
+  a.n_mblk = (a.M + C::FEATS - 1) / C::FEATS;
+  // tiles at most: each non-empty segment adds at most one partial row block
+  const long long most = (static_cast<long long>(a.rows + 255) / 256 + a.groups) * a.n_mblk;
+  const int pairs = num_sms / 2 < most ? num_sms / 2 : static_cast<int>(most);
+  train_gemm_kernel<MODE, SUBS><<<2 * pairs, C::THREADS, smem, stream>>>(tmA, tmB, a);
   return cudaGetLastError();
+}
+cudaError_t launch_train_gemm(int mode, int subs, const CUtensorMap& tmA, const HalfMaps& tmB, const TrainGemmArgs& a,
+                              int num_sms, cudaStream_t stream) {
+  return mode == TRAIN_FORWARD  ? train_gemm<TRAIN_FORWARD, 2>(tmA, tmB, a, num_sms, stream)
+         : mode == TRAIN_HIDDEN ? train_gemm<TRAIN_HIDDEN, 1>(tmA, tmB, a, num_sms, stream)
+         : subs == 2            ? train_gemm<TRAIN_ROWS, 2>(tmA, tmB, a, num_sms, stream)
+                                : train_gemm<TRAIN_ROWS, 1>(tmA, tmB, a, num_sms, stream);
 }
 
 cudaError_t launch_row_w_grad(int rows, int n, const float* partial, const int32_t* offsets, int groups, float* d_row_w,

@@ -5,8 +5,7 @@
 
 namespace moe {
 
-// The training GEMMs over expert segments, one tile scheme (256 weight-side
-// rows by up to 256 token rows):
+// The training GEMMs over expert segments (train_gemm_kernel):
 //   TRAIN_FORWARD  [g | u] = B w13^T, h = SiLU(g) * u; gu and h stored. K = H, M = I
 //   TRAIN_HIDDEN   dh0 = B w2 (B = d_out), then the activation's backward. K = H, M = I
 //   TRAIN_ROWS     out = B W (+ add), W [groups, K, M] row-major or tiled w13
@@ -14,7 +13,7 @@ enum { TRAIN_FORWARD = 0, TRAIN_HIDDEN = 1, TRAIN_ROWS = 2 };
 struct TrainGemmArgs {
   int32_t rows = 0, K = 0, M = 0, groups = 1;
   const int32_t* offsets = nullptr;   // [groups + 1] or nullptr (one segment)
-  int32_t n_mblk = 0;                 // feature blocks: 128 (forward), 256 (else; the last may hold 128)
+  int32_t n_mblk = 0;                 // feature blocks per group (set by the launcher)
   int32_t tiled = 0;                  // W in moe_tile_ffn_weights' layout
   __nv_bfloat16* gu = nullptr;        // [rows, 2I]: forward out, hidden in
   __nv_bfloat16* h = nullptr;         // [rows, I] out: forward h, hidden row_w * h
@@ -26,8 +25,14 @@ struct TrainGemmArgs {
   int32_t* status = nullptr;
   uint64_t wait_ns = kDefaultWaitLimitNs;
 };
-cudaError_t launch_train_gemm(int mode, const CUtensorMap& tmA, const TokenMaps& tmB, const TrainGemmArgs& a, int grid,
-                              cudaStream_t stream);
+// Half of a tile's token rows: box[i] has 16 (i + 1) rows.
+struct HalfMaps {
+  CUtensorMap box[8];
+};
+// Sub-tiles per CTA of a product of K terms (see train_gemm_kernel).
+inline int train_subs(int mode, int K) { return mode == TRAIN_FORWARD || (mode == TRAIN_ROWS && K > 512) ? 2 : 1; }
+cudaError_t launch_train_gemm(int mode, int subs, const CUtensorMap& tmA, const HalfMaps& tmB, const TrainGemmArgs& a,
+                              int num_sms, cudaStream_t stream);
 cudaError_t launch_row_w_grad(int rows, int n, const float* partial, const int32_t* offsets, int groups, float* d_row_w,
                               cudaStream_t stream);
 
@@ -35,10 +40,10 @@ cudaError_t launch_row_w_grad(int rows, int n, const float* partial, const int32
 // products over the same segments in one launch.
 struct WgradProblem {
   CUtensorMap tmA, tmB;               // [rows, M], [rows, N] bf16 as column blocks: 64 rows x 2 blocks of 64
-  CUtensorMap tmOut;                  // [groups * M, N], boxes of 32 rows x 128 bytes
+  CUtensorMap tmOut;                  // [groups * M, N] bf16 or fp32, boxes of 32 rows x 128 bytes
   int32_t M, N, tiles;                // tiles = groups * per_group
   int32_t a_flat;                     // M % 64 != 0: tmA is the plain matrix, boxes of 64 rows x 64 columns
-  int32_t per_group, n_blocks;        // tiles of a group; its blocks along N
+  int32_t per_group, m_blocks, n_blocks;   // tiles of a group; its blocks along M and N
 };
 struct WgradArgs {
   WgradProblem prob[2];

@@ -151,6 +151,21 @@ def test_backward_long_segments_and_one_group():
     _check(o, c, off, H, I)
 
 
+@pytest.mark.parametrize("f32", [False, True])
+def test_backward_many_experts_of_all_lengths(f32):
+    """Enough experts that a pair of SMs takes runs of weight-gradient tiles,
+    with segments that fit (at most 384 rows), that do not, that end anywhere in
+    a K step, and that are empty, next to one another."""
+    counts = [0, 1, 15, 16, 17, 63, 64, 65, 128, 384, 385, 0, 200, 383, 400, 31, 320, 321, 48, 449, 2, 0, 96, 333]
+    H, I = 1024, 1408
+    c, off, R, E = _case(counts, H, I, seed=21)
+    o = _backward(c, off, R, E, H, I, f32=f32)
+    _check(o, c, off, H, I)
+    again = _backward(c, off, R, E, H, I, f32=f32)
+    for k, v in o.items():
+        assert torch.equal(v, again[k])
+
+
 def test_backward_outputs_on_their_own_and_twice():
     """Each output alone is what it is among all; two calls agree bit for bit."""
     H, I = 256, 384
