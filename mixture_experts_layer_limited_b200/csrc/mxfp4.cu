@@ -78,6 +78,8 @@ constexpr int kMxRows = 8;                                           // rows (wa
 __global__ void __launch_bounds__(32 * kMxRows)
 mx_quant_rows_kernel(int rows, int K, const uint4* __restrict__ a, int a_rows, const int32_t* __restrict__ src,
                      uint32_t* __restrict__ q, uint32_t* __restrict__ scale, int32_t* status) {
+  launch_dependents_if_small();
+  griddep_wait();
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.x * kMxRows + (threadIdx.x >> 5);
   if (r >= rows) return;                                             // warp-uniform
@@ -129,6 +131,8 @@ __device__ __forceinline__ uint32_t mx_bf16x2(uint32_t codes, float sc) {
 __global__ void __launch_bounds__(32 * kMxRows)
 mx_dequant_rows_kernel(int rows, int K, const uint32_t* __restrict__ q, const uint32_t* __restrict__ scale,
                        uint4* __restrict__ out) {
+  launch_dependents_if_small();
+  griddep_wait();
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.x * kMxRows + (threadIdx.x >> 5);
   if (r >= rows) return;
@@ -278,6 +282,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     tmem_alloc(&tmem_base_s, 512);
     tmem_relinquish();
   }
+  griddep_launch_dependents();
+  griddep_wait();
   if (warp == 3) build_schedule(sched, sp, lane);
   tc_fence_before();
   __syncthreads();
@@ -508,20 +514,18 @@ cudaError_t launch_mx_gemm(bool gate_up, const CUtensorMap& tmA, const TokenMaps
   auto kern = gate_up ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kern<<<grid, kMxThreads, smem, stream>>>(tmA, tmB, a);
-  return cudaGetLastError();
+  return launch_after(kern, grid, kMxThreads, smem, stream, tmA, tmB, a);
 }
 
 cudaError_t launch_mx_quant_rows(int rows, int K, const void* a, int a_rows, const int32_t* src, void* q, void* scale,
                                  int32_t* status, cudaStream_t stream) {
-  mx_quant_rows_kernel<<<(rows + kMxRows - 1) / kMxRows, 32 * kMxRows, 0, stream>>>(
-      rows, K, static_cast<const uint4*>(a), a_rows, src, static_cast<uint32_t*>(q), static_cast<uint32_t*>(scale), status);
-  return cudaGetLastError();
+  return launch_after(mx_quant_rows_kernel, (rows + kMxRows - 1) / kMxRows, 32 * kMxRows, 0, stream, rows, K,
+                      static_cast<const uint4*>(a), a_rows, src, static_cast<uint32_t*>(q), static_cast<uint32_t*>(scale),
+                      status);
 }
 cudaError_t launch_mx_dequant_rows(int rows, int K, const void* q, const void* scale, void* out, cudaStream_t stream) {
-  mx_dequant_rows_kernel<<<(rows + kMxRows - 1) / kMxRows, 32 * kMxRows, 0, stream>>>(
-      rows, K, static_cast<const uint32_t*>(q), static_cast<const uint32_t*>(scale), static_cast<uint4*>(out));
-  return cudaGetLastError();
+  return launch_after(mx_dequant_rows_kernel, (rows + kMxRows - 1) / kMxRows, 32 * kMxRows, 0, stream, rows, K,
+                      static_cast<const uint32_t*>(q), static_cast<const uint32_t*>(scale), static_cast<uint4*>(out));
 }
 cudaError_t launch_mx_quant_weights(int batch, int N, int K, const void* w, void* q, void* scale, cudaStream_t stream) {
   const long long n = static_cast<long long>(batch) * N;

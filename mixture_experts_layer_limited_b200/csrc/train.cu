@@ -275,6 +275,8 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     for (int i = 0; i < 8; ++i) tma_prefetch_desc(&tmB.box[i]);
   }
   if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 512);
+  griddep_launch_dependents();
+  griddep_wait();
   if (warp == 2) build_schedule(sm.sched, sp, lane);
   tc_fence_before();
   __syncthreads();
@@ -483,6 +485,8 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 __global__ void __launch_bounds__(256)
 row_w_grad_kernel(int rows, int n, const float* __restrict__ partial, const int32_t* __restrict__ offsets, int groups,
                   float* __restrict__ d_row_w) {
+  launch_dependents_if_small();
+  griddep_wait();
   const int r = blockIdx.x * 256 + threadIdx.x;
   const int lo = offsets ? offsets[0] : 0, hi = offsets ? offsets[groups] : rows;   // r < rows bounds both
   if (r >= rows || r < lo || r >= hi) return;
@@ -604,8 +608,6 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int first = static_cast<int>(cluster_id_x()), stride = static_cast<int>(gridDim.x) / 2;
-  for (int i = threadIdx.x; i <= a.groups; i += blockDim.x)
-    sm.off[i] = a.offsets ? min(max(a.offsets[i], 0), a.rows) : i * a.rows;
   auto sA = [&](int st) { return sm.stage[st]; };
   auto sB = [&](int st) { return sm.stage[st] + C::PAIR; };
 
@@ -634,6 +636,10 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
     }
   }
   if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 512);
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int i = threadIdx.x; i <= a.groups; i += blockDim.x)
+    sm.off[i] = a.offsets ? min(max(a.offsets[i], 0), a.rows) : i * a.rows;
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                                  // both CTAs' barriers and TMEM are ready
@@ -853,6 +859,8 @@ route_backward_kernel(int T, int E, int k, int scoring, int norm, float scale, c
                       const int32_t* __restrict__ slot_to_row, float* __restrict__ d_logits,
                       __nv_bfloat16* __restrict__ d_logits16, int32_t* status) {
   constexpr int PER = 8;                                           // E <= 256
+  launch_dependents_if_small();
+  griddep_wait();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (t >= T) return;
@@ -944,8 +952,7 @@ static cudaError_t train_gemm(const CUtensorMap& tmA, const HalfMaps& tmB, Train
   // tiles at most: each non-empty segment adds at most one partial row block
   const long long most = (static_cast<long long>(a.rows + 255) / 256 + a.groups) * a.n_mblk;
   const int pairs = num_sms / 2 < most ? num_sms / 2 : static_cast<int>(most);
-  train_gemm_kernel<MODE, SUBS><<<2 * pairs, C::THREADS, smem, stream>>>(tmA, tmB, a);
-  return cudaGetLastError();
+  return launch_after(train_gemm_kernel<MODE, SUBS>, 2 * pairs, C::THREADS, smem, stream, tmA, tmB, a);
 }
 cudaError_t launch_train_gemm(int mode, int subs, const CUtensorMap& tmA, const HalfMaps& tmB, const TrainGemmArgs& a,
                               int num_sms, cudaStream_t stream) {
@@ -957,16 +964,14 @@ cudaError_t launch_train_gemm(int mode, int subs, const CUtensorMap& tmA, const 
 
 cudaError_t launch_row_w_grad(int rows, int n, const float* partial, const int32_t* offsets, int groups, float* d_row_w,
                               cudaStream_t stream) {
-  row_w_grad_kernel<<<(rows + 255) / 256, 256, 0, stream>>>(rows, n, partial, offsets, groups, d_row_w);
-  return cudaGetLastError();
+  return launch_after(row_w_grad_kernel, (rows + 255) / 256, 256, 0, stream, rows, n, partial, offsets, groups, d_row_w);
 }
 
 cudaError_t launch_route_backward(int T, int E, int k, int scoring, int norm, float scale, const float* logits,
                                   const int32_t* ids, const float* d_w, const int32_t* slot_to_row, float* d_logits,
                                   void* d_logits16, int32_t* status, cudaStream_t stream) {
-  route_backward_kernel<<<(T + 7) / 8, 256, 0, stream>>>(T, E, k, scoring, norm, scale, logits, ids, d_w, slot_to_row,
-                                                         d_logits, reinterpret_cast<__nv_bfloat16*>(d_logits16), status);
-  return cudaGetLastError();
+  return launch_after(route_backward_kernel, (T + 7) / 8, 256, 0, stream, T, E, k, scoring, norm, scale, logits, ids, d_w,
+                      slot_to_row, d_logits, static_cast<__nv_bfloat16*>(d_logits16), status);
 }
 
 cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
@@ -976,8 +981,7 @@ cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int tiles = a.prob[0].tiles + (a.n_prob > 1 ? a.prob[1].tiles : 0);
   const int pairs = num_sms / 2 < tiles ? num_sms / 2 : tiles;
-  wgrad_kernel<<<2 * pairs, WgradCfg::THREADS, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(wgrad_kernel, 2 * pairs, WgradCfg::THREADS, smem, stream, a);
 }
 
 }  // namespace moe

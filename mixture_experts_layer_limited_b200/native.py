@@ -139,7 +139,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle of a device; torch.cuda.current_stream() builds a
+# Stream object for it, 3 of the 10 us a small call takes on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -153,17 +160,23 @@ def _check(fn: str, status: int):
         raise MoEError(fn, status, detail)
 
 
-def _expect(fn: str, **tensors):
-    """name=(tensor or None, elements, dtype): device, type and size of a call's
-    tensors, checked before any pointer is passed on."""
+def _tensors(fn, *specs):
+    """(name, tensor or None, elements, dtype) -> device pointers, after a check
+    of every tensor's device, type, layout and size."""
     dev = torch.cuda.current_device()
-    for name, (t, n, dtype) in tensors.items():
+    out = []
+    for name, t, n, dtype in specs:
         if t is None:
+            out.append(None)
             continue
-        if t.dtype != dtype or t.numel() < n:
+        if t.dtype is not dtype or t.numel() < n:
             raise ValueError(f"{fn}: {name} has {t.numel()} elements of {t.dtype}, expected {n} of {dtype}")
-        if t.device.index != dev:
+        if t.get_device() != dev:
             raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} is not contiguous")
+        out.append(t.data_ptr())
+    return out
 
 
 # ---------------------------------------------------------------- the ABI
@@ -320,12 +333,12 @@ def moe_gate_up_swiglu_train(rows, H, w13, groups, I, a, offsets, h, gu, dev_sta
                              tiled=False):
     """moe_gate_up_swiglu that also stores the pre-activations gu [rows, 2I]."""
     bf = torch.bfloat16
-    _expect("moe_gate_up_swiglu_train", w13=(w13, groups * 2 * I * H, bf), a=(a, rows * H, bf),
-            offsets=(offsets, groups + 1, torch.int32), h=(h, rows * I, bf), gu=(gu, rows * 2 * I, bf))
-    w = FFNWeights(_ptr(w13), None, None, None, MOE_BF16, groups, I)
-    w.tiled = int(tiled)
+    p13, pa, poff, ph, pgu = _tensors(
+        "moe_gate_up_swiglu_train", ("w13", w13, groups * 2 * I * H, bf), ("a", a, rows * H, bf),
+        ("offsets", offsets, groups + 1, torch.int32), ("h", h, rows * I, bf), ("gu", gu, rows * 2 * I, bf))
+    w = FFNWeights(p13, None, None, None, MOE_BF16, groups, I, int(tiled))
     _check("moe_gate_up_swiglu_train", load_library().moe_gate_up_swiglu_train(
-        rows, H, ctypes.byref(w), _ptr(a), _ptr(offsets), _ptr(h), _ptr(gu), _ptr(dev_status), _stream(stream)))
+        rows, H, ctypes.byref(w), pa, poff, ph, pgu, _ptr(dev_status), _stream(stream)))
 
 
 def moe_swiglu_ffn_backward_workspace_size(rows, I) -> int:
@@ -341,39 +354,40 @@ def moe_swiglu_ffn_backward(rows, H, w13, w2, groups, I, a, gu, d_out, offsets, 
     """Gradients of the experts' block at the pre-activations gu that
     moe_gate_up_swiglu_train saved; outputs that are None are not computed."""
     bf, f32, gt = torch.bfloat16, torch.float32, _grad("moe_swiglu_ffn_backward", grad_dtype)
-    _expect("moe_swiglu_ffn_backward", w13=(w13, groups * 2 * I * H, bf), w2=(w2, groups * H * I, bf),
-            a=(a, rows * H, bf), gu=(gu, rows * 2 * I, bf), d_out=(d_out, rows * H, bf),
-            offsets=(offsets, groups + 1, torch.int32), row_w=(row_w, rows, f32), d_a=(d_a, rows * H, bf),
-            d_w13=(d_w13, groups * 2 * I * H, gt), d_w2=(d_w2, groups * H * I, gt), d_row_w=(d_row_w, rows, f32))
-    w = FFNWeights(_ptr(w13), _ptr(w2), None, None, MOE_BF16, groups, I)
-    w.tiled = int(tiled)
+    n13, n2 = groups * 2 * I * H, groups * H * I
+    p13, p2, pa, pgu, pdo, poff, prw, pda, pd13, pd2, pdrw = _tensors(
+        "moe_swiglu_ffn_backward", ("w13", w13, n13, bf), ("w2", w2, n2, bf), ("a", a, rows * H, bf),
+        ("gu", gu, rows * 2 * I, bf), ("d_out", d_out, rows * H, bf), ("offsets", offsets, groups + 1, torch.int32),
+        ("row_w", row_w, rows, f32), ("d_a", d_a, rows * H, bf), ("d_w13", d_w13, n13, gt), ("d_w2", d_w2, n2, gt),
+        ("d_row_w", d_row_w, rows, f32))
+    w = FFNWeights(p13, p2, None, None, MOE_BF16, groups, I, int(tiled))
     _check("moe_swiglu_ffn_backward", load_library().moe_swiglu_ffn_backward(
-        rows, H, ctypes.byref(w), _ptr(a), _ptr(gu), _ptr(d_out), _ptr(offsets), _ptr(row_w), _ptr(d_a),
-        _ptr(d_w13), _ptr(d_w2), grad_dtype, int(bool(accumulate)), _ptr(d_row_w), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
+        rows, H, ctypes.byref(w), pa, pgu, pdo, poff, prw, pda, pd13, pd2, grad_dtype, int(bool(accumulate)), pdrw,
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
 
 
 def moe_route_backward(T, E, k, scoring, norm_topk_prob, routed_scaling_factor, logits, topk_ids, d_topk_w,
                        slot_to_row, d_logits, d_logits_bf16=None, dev_status=None, stream=None):
     """d_topk_w in slot order (slot_to_row None), or in row order with it."""
     f32, i32 = torch.float32, torch.int32
-    _expect("moe_route_backward", logits=(logits, T * E, f32), topk_ids=(topk_ids, T * k, i32),
-            d_topk_w=(d_topk_w, T * k, f32), slot_to_row=(slot_to_row, T * k, i32), d_logits=(d_logits, T * E, f32),
-            d_logits_bf16=(d_logits_bf16, T * E, torch.bfloat16))
+    pl, pids, pdw, ps2r, pout, p16 = _tensors(
+        "moe_route_backward", ("logits", logits, T * E, f32), ("topk_ids", topk_ids, T * k, i32),
+        ("d_topk_w", d_topk_w, T * k, f32), ("slot_to_row", slot_to_row, T * k, i32), ("d_logits", d_logits, T * E, f32),
+        ("d_logits_bf16", d_logits_bf16, T * E, torch.bfloat16))
     _check("moe_route_backward", load_library().moe_route_backward(
-        T, E, k, scoring, int(bool(norm_topk_prob)), float(routed_scaling_factor), _ptr(logits), _ptr(topk_ids),
-        _ptr(d_topk_w), _ptr(slot_to_row), _ptr(d_logits), _ptr(d_logits_bf16), _ptr(dev_status), _stream(stream)))
+        T, E, k, scoring, int(bool(norm_topk_prob)), float(routed_scaling_factor), pl, pids, pdw, ps2r, pout, p16,
+        _ptr(dev_status), _stream(stream)))
 
 
 def moe_gate_backward(T, H, E, d_logits_bf16, x, gate_w, dx_in, dx, d_gate, grad_dtype=MOE_BF16, accumulate=False,
                       dev_status=None, stream=None):
     """dx = dx_in + d_logits gate and d_gate = d_logits^T x; either may be None."""
     bf, gt = torch.bfloat16, _grad("moe_gate_backward", grad_dtype)
-    _expect("moe_gate_backward", d_logits_bf16=(d_logits_bf16, T * E, bf), x=(x, T * H, bf), gate_w=(gate_w, E * H, bf),
-            dx_in=(dx_in, T * H, bf), dx=(dx, T * H, bf), d_gate=(d_gate, E * H, gt))
+    pdl, px, pg, pin, pdx, pdg = _tensors(
+        "moe_gate_backward", ("d_logits_bf16", d_logits_bf16, T * E, bf), ("x", x, T * H, bf), ("gate_w", gate_w, E * H, bf),
+        ("dx_in", dx_in, T * H, bf), ("dx", dx, T * H, bf), ("d_gate", d_gate, E * H, gt))
     _check("moe_gate_backward", load_library().moe_gate_backward(
-        T, H, E, _ptr(d_logits_bf16), _ptr(x), _ptr(gate_w), _ptr(dx_in), _ptr(dx), _ptr(d_gate), grad_dtype,
-        int(bool(accumulate)), _ptr(dev_status), _stream(stream)))
+        T, H, E, pdl, px, pg, pin, pdx, pdg, grad_dtype, int(bool(accumulate)), _ptr(dev_status), _stream(stream)))
 
 
 def moe_combine(T, k, H, expert_out, slot_to_row, topk_w, shared_out, y, stream=None):
@@ -416,29 +430,28 @@ def moe_quantize_mxfp4_rows(rows, K, a, a_rows, src_rows, q, scale, dev_status=N
     """Rows src_rows of a (None: its first rows) as 4-bit codes q [rows, K/2]
     (uint8) and scales [K/128, rows, 4] (uint8)."""
     u8 = torch.uint8
-    _expect("moe_quantize_mxfp4_rows", a=(a, a_rows * K, torch.bfloat16), src_rows=(src_rows, rows, torch.int32),
-            q=(q, rows * K // 2, u8), scale=(scale, rows * K // 32, u8))
+    pa, psrc, pq, ps = _tensors(
+        "moe_quantize_mxfp4_rows", ("a", a, a_rows * K, torch.bfloat16), ("src_rows", src_rows, rows, torch.int32),
+        ("q", q, rows * K // 2, u8), ("scale", scale, rows * K // 32, u8))
     _check("moe_quantize_mxfp4_rows", load_library().moe_quantize_mxfp4_rows(
-        rows, K, _ptr(a), a_rows, _ptr(src_rows), _ptr(q), _ptr(scale), _ptr(dev_status), _stream(stream)))
+        rows, K, pa, a_rows, psrc, pq, ps, _ptr(dev_status), _stream(stream)))
 
 
 def moe_dequantize_mxfp4_rows(rows, K, q, scale, out, stream=None):
     """The bf16 values of moe_quantize_mxfp4_rows' codes."""
     u8 = torch.uint8
-    _expect("moe_dequantize_mxfp4_rows", q=(q, rows * K // 2, u8), scale=(scale, rows * K // 32, u8),
-            out=(out, rows * K, torch.bfloat16))
-    _check("moe_dequantize_mxfp4_rows", load_library().moe_dequantize_mxfp4_rows(
-        rows, K, _ptr(q), _ptr(scale), _ptr(out), _stream(stream)))
+    pq, ps, po = _tensors("moe_dequantize_mxfp4_rows", ("q", q, rows * K // 2, u8), ("scale", scale, rows * K // 32, u8),
+                          ("out", out, rows * K, torch.bfloat16))
+    _check("moe_dequantize_mxfp4_rows", load_library().moe_dequantize_mxfp4_rows(rows, K, pq, ps, po, _stream(stream)))
 
 
 def moe_quantize_mxfp4_weights(batch, N, K, w, q, scale, stream=None):
     """Weights w [batch, N, K] as codes q [batch, N, K/2] and scales
     [batch, N/128, K/128, 512] (uint8), as the MOE_MXFP4 products take them."""
     u8 = torch.uint8
-    _expect("moe_quantize_mxfp4_weights", w=(w, batch * N * K, torch.bfloat16), q=(q, batch * N * K // 2, u8),
-            scale=(scale, batch * N * K // 32, u8))
-    _check("moe_quantize_mxfp4_weights", load_library().moe_quantize_mxfp4_weights(
-        batch, N, K, _ptr(w), _ptr(q), _ptr(scale), _stream(stream)))
+    pw, pq, ps = _tensors("moe_quantize_mxfp4_weights", ("w", w, batch * N * K, torch.bfloat16),
+                          ("q", q, batch * N * K // 2, u8), ("scale", scale, batch * N * K // 32, u8))
+    _check("moe_quantize_mxfp4_weights", load_library().moe_quantize_mxfp4_weights(batch, N, K, pw, pq, ps, _stream(stream)))
 
 
 def moe_read_device_status(dev_status, stream=None) -> int:
