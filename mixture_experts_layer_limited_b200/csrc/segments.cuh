@@ -28,9 +28,9 @@ constexpr int kTbChunk = 8;
 // memory. The training and 4-bit calls are chains of such kernels, a few
 // microseconds each where rows are few.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), int grid, int block, size_t smem, cudaStream_t stream, A&&... args) {
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int block, size_t smem, cudaStream_t stream, A&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(block));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -47,7 +47,7 @@ cudaError_t launch_after(void (*kern)(P...), int grid, int block, size_t smem, c
 // each SM has one CTA at most; beside more of them its CTAs would take the free
 // places unevenly (4096 rows to 4 bits and back: 60 us instead of 48).
 __device__ __forceinline__ void launch_dependents_if_small() {
-  if (gridDim.x <= 148) griddep_launch_dependents();
+  if (gridDim.x * gridDim.y <= 148) griddep_launch_dependents();
 }
 
 // A grouped GEMM as the schedule sees it.
