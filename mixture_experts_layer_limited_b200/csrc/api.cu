@@ -407,9 +407,9 @@ moe_status launch_plan(const GemmPlan& p, int epi, cudaStream_t st, int nsm, con
 }
 
 // Rows per tile and pipeline stages of the 4-bit GEMMs, by the rows an expert
-// has on average. A small tile leaves room for a fourth stage of weights in
-// flight, which is what counts at a few rows per expert; twice the average, so
-// that most segments still fit one tile and their weights are read once.
+// has on average. A small tile leaves room for more stages of weights in flight,
+// which is what counts at a few rows per expert; twice the average, so that most
+// segments still fit one tile and their weights are read once.
 void mx_tile(int32_t rows, int32_t groups, MxGemmArgs* g) {
   const int32_t twice = 2 * ((rows + groups - 1) / groups);
   g->bn_max = twice <= 32 ? 32 : twice <= 64 ? 64 : 192;

@@ -47,27 +47,33 @@ __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float inv) {
 // |v|, with NaN as infinity, so that a maximum over a block keeps either
 __device__ __forceinline__ float mx_mag(float v) { return v != v ? INFINITY : fabsf(v); }
 
-__device__ __forceinline__ void bf16x8(const uint4& u, float (&f)[8]) {
+// Four lanes hold a block of 32 values, eight each: its scale byte and this
+// lane's codes. The largest magnitude and the scaling run on pairs of bf16 (the
+// maximum keeps NaN; a power of two scales exactly, and what falls below bf16's
+// smallest number is far below half a code).
+__device__ __forceinline__ uint32_t mx_block(const uint4& u, uint32_t& scale) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  auto pair = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+  __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(__habs2(pair(w[0])), __habs2(pair(w[1]))),
+                                  __hmax2_nan(__habs2(pair(w[2])), __habs2(pair(w[3]))));
+  uint32_t m = *reinterpret_cast<const uint32_t*>(&m2);
+#pragma unroll
+  for (int d = 1; d <= 2; d <<= 1) {
+    m2 = __hmax2_nan(pair(m), pair(__shfl_xor_sync(0xffffffffu, m, d)));
+    m = *reinterpret_cast<const uint32_t*>(&m2);
+  }
+  const float amax = __bfloat162float(__hmax_nan(__low2bfloat16(m2), __high2bfloat16(m2)));
+  scale = mx_scale_of(amax);
+  const __nv_bfloat162 inv = __float2bfloat162_rn(mx_inv_scale(scale));
+  float f[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const __nv_bfloat162 p = __hmul2(pair(w[i]), inv);
+    const uint32_t x = *reinterpret_cast<const uint32_t*>(&p);
+    f[2 * i] = __uint_as_float(x << 16);
+    f[2 * i + 1] = __uint_as_float(x & 0xffff0000u);
   }
-}
-
-// Four lanes hold a block of 32 values, eight each: its scale byte and this
-// lane's codes.
-__device__ __forceinline__ uint32_t mx_block(const uint4& u, uint32_t& scale) {
-  float f[8];
-  bf16x8(u, f);
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, mx_mag(f[i]));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  scale = mx_scale_of(m);
-  return mx_codes8(f, mx_inv_scale(scale));
+  return mx_codes8(f, 1.0f);
 }
 
 // ---------------------------------------------------------------- rows
@@ -188,12 +194,17 @@ mx_quant_weights_kernel(long long n_rows, int N, int K, const uint4* __restrict_
 }
 
 // ---------------------------------------------------------------- product
-// 32 rows x 16 bytes of shared memory into 4 TMEM columns, all lane quarters.
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem_addr) {
-  // no swizzle, groups of 8 rows 128 B apart
-  const uint64_t d = static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1u) << 16 |
-                     static_cast<uint64_t>(128u >> 4) << 32 | static_cast<uint64_t>(1u) << 46;
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+// 32 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
 }
 __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
@@ -219,21 +230,23 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
 }
 
 constexpr int kMxEpi = 8;                                            // epilogue warps
-constexpr int kMxThreads = 32 * (4 + kMxEpi);
+constexpr int kMxThreads = 32 * (8 + kMxEpi);
 constexpr int kMxMaxStages = 4;
 constexpr uint32_t kMxA = 256 * 128;                                 // 256 weight rows x 256 values
-constexpr uint32_t kMxSfa = 2048, kMxSfb = 2048;
-__host__ __device__ constexpr uint32_t mx_stage_bytes(int bn) { return kMxA + static_cast<uint32_t>(bn) * 128u + kMxSfa + kMxSfb; }
+constexpr uint32_t kMxSfa = 2048;                                    // their scales
+__host__ __device__ constexpr uint32_t mx_stage_bytes(int bn) { return kMxA + kMxSfa + static_cast<uint32_t>(bn) * 128u; }
 
 // Tiles as in the forward GEMMs: 256 weight rows (gate and up rows of 128
 // features, or 256 rows of w2) as the MMA's A, up to bn_max rows of a segment
 // as B, accumulated side by side in TMEM columns [0, bn) and [bn, 2 bn). A
-// stage is 256 values of K: the codes by TMA, the weights' scales as one or two
-// 512-byte blocks per 128 rows by a bulk copy, and the rows' scales, which lie
-// row by row at any offset, arranged the same way by warp 2. The MMA thread
-// copies the scales to TMEM columns of the stage's own (2 bn + 32 * stage ...),
-// so no copy meets MMAs still reading the last ones.
-//   warp 0 TMA, warp 1 TMEM and MMAs, warp 2 the rows' scales, warps 4..11 the
+// stage is 256 values of K: the codes by TMA into shared memory, the weights'
+// scales by bulk copies beside them, the rows' from L2. Four warps, one for each
+// quarter of the TMEM lanes, then write all scales to 32 TMEM columns of the
+// stage's own (2 bn + 32 * stage ..): lane l of column c has the word (four
+// scales, 128 values) of row 32 c + l, the same in all four quarters. (Copied
+// from shared memory by tcgen05.cp, which the MMAs wait for in line, 8 rows on
+// each of 64 V3 experts took 268 us.)
+//   warp 0 TMA, warp 1 TMEM and MMAs, warps 4..7 the scales, warps 8..15 the
 //   epilogue: gate/up quantises h = SiLU(g) u, a warp's 32 features being one
 //   block of 32, through a shared tile so that a lane has one row's block.
 // At a few rows per expert the weights' bytes bound it (4.25 bits a value).
@@ -243,10 +256,10 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   extern __shared__ __align__(1024) uint8_t dsmem[];
   __shared__ SegSched sched;
   __shared__ __align__(16) float tile_s[kMxEpi][32 * 33];
-  __shared__ uint64_t full_bar[kMxMaxStages], empty_bar[kMxMaxStages];
+  __shared__ uint64_t full_bar[kMxMaxStages], sfa_bar[kMxMaxStages], scaled_bar[kMxMaxStages], empty_bar[kMxMaxStages];
   __shared__ uint64_t tmem_full, tmem_empty, drain_bar;
   __shared__ uint32_t tmem_base_s;
-  __shared__ int issued_parity[kMxMaxStages], scaled_parity[kMxMaxStages];   // last phase of the loads', of warp 2's arrival
+  __shared__ int issued_parity[kMxMaxStages];
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -257,14 +270,15 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   auto sA = [&](int st) { return smem + st * stage_bytes; };
   auto sB = [&](int st) { return smem + st * stage_bytes + kMxA; };
   auto sSfa = [&](int st) { return smem + st * stage_bytes + kMxA + bn * 128u; };
-  auto sSfb = [&](int st) { return smem + st * stage_bytes + kMxA + bn * 128u + kMxSfa; };
   const SegProblem sp{a.rows, a.groups, a.offsets, a.n_mblk, a.bn_max, 16, a.status};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMxMaxStages; ++i) {
-      mbar_init(&full_bar[i], 2);                                    // the loads' and warp 2's
+      mbar_init(&full_bar[i], 1);                                    // the codes have landed
+      mbar_init(&sfa_bar[i], 1);                                     // the weights' scales have
+      mbar_init(&scaled_bar[i], 4);                                  // the scale warps have written TMEM
       mbar_init(&empty_bar[i], 1);
-      issued_parity[i] = scaled_parity[i] = -1;
+      issued_parity[i] = -1;
     }
     mbar_init(&tmem_full, 1);
     mbar_init(&tmem_empty, 32 * kMxEpi);
@@ -311,63 +325,64 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag, a.status, a.wait_ns)) { ok = false; break; }
           uint64_t* fb = &full_bar[stage];
           const uint32_t sf_bytes = k128 - 2 * kb >= 2 ? 1024u : 512u;
-          mbar_arrive_expect_tx(fb, kMxA + static_cast<uint32_t>(ti.N) * 128u + 2 * sf_bytes);
+          mbar_arrive_expect_tx(&sfa_bar[stage], 2 * sf_bytes);
+          bulk_load(sSfa(stage), sf0 + kb * 1024, sf_bytes, &sfa_bar[stage]);
+          bulk_load(sSfa(stage) + 1024, sf1 + kb * 1024, sf_bytes, &sfa_bar[stage]);
+          mbar_arrive_expect_tx(fb, kMxA + static_cast<uint32_t>(ti.N) * 128u);
           tma_load_2d(sA(stage), &tmA, fb, kb * 128, row0, pol_w);
           if (!a.a_one_box) tma_load_2d(sA(stage) + 128 * 128, &tmA, fb, kb * 128, row1, pol_w);
           uint8_t* bdst = sB(stage);
           load_token_rows(ti.N, [&](int which, int off) {
             tma_load_2d(bdst + off * 128, &tmB.box[which], fb, kb * 128, ti.row0 + off, pol_x);
           });
-          bulk_load(sSfa(stage), sf0 + kb * 1024, sf_bytes, fb);
-          bulk_load(sSfa(stage) + 1024, sf1 + kb * 1024, sf_bytes, fb);
           issued_parity[stage] = static_cast<int>(phase);
           if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
       }
     }
-  } else if (warp == 2) {
-    // the rows' scales: word of row r and block kk at b_scale[kk * rows + r],
-    // to (r % 32) * 16 + (r / 32 % 4) * 4 of a 512-byte block per 128 rows
+  } else if (warp >= 4 && warp < 8) {
+    const int q = warp & 3;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     int g = 0;
     for (int t = blockIdx.x; t < total && ok && !abort_flag; t += gridDim.x) {
       const SegTile ti = decode_tile(sched, sp, t, g);
-      const int nrb = (ti.N + 127) / 128;
-      uint32_t w[2][2][4];
+      // columns [A0 kh0: 4][A0 kh1: 4][A1: 8][B kh0: 8][B kh1: 8]
+      uint32_t x[16];                                                // the rows' words of the next block
       auto fetch = [&](int kb) {
 #pragma unroll
-        for (int kh = 0; kh < 2; ++kh)
+        for (int kh = 0; kh < 2; ++kh) {
+          const int kk = 2 * kb + kh;
 #pragma unroll
-          for (int rb = 0; rb < 2; ++rb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int r = rb * 128 + c * 32 + lane;                // rows behind the tile's: scale 1, not used
-              w[kh][rb][c] = r < ti.n_valid && 2 * kb + kh < k128
-                                 ? __ldg(a.b_scale + static_cast<size_t>(2 * kb + kh) * a.rows + ti.row0 + r) : 0x7f7f7f7fu;
-            }
+          for (int c = 0; c < 8; ++c) {
+            const int r = c * 32 + lane;                             // rows behind the tile's: scale 1, not used
+            x[8 * kh + c] = kk < k128 && r < ti.n_valid
+                                ? __ldg(a.b_scale + static_cast<size_t>(kk) * a.rows + ti.row0 + r) : 0x7f7f7f7fu;
+          }
+        }
       };
       fetch(0);
       for (int kb = 0; kb < nk; ++kb) {
-        ok = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, &abort_flag, a.status, a.wait_ns);
+        ok = mbar_wait_warp(&sfa_bar[stage], phase, &abort_flag, a.status, a.wait_ns);
         if (!ok) break;
-        uint8_t* dst = sSfb(stage);
+        uint32_t w[32];
+        const uint4* sf = reinterpret_cast<const uint4*>(sSfa(stage)) + lane;
 #pragma unroll
-        for (int kh = 0; kh < 2; ++kh)
-#pragma unroll
-          for (int rb = 0; rb < 2; ++rb)
-            if (rb < nrb)
-              *reinterpret_cast<uint4*>(dst + (kh * 2 + rb) * 512 + lane * 16) =
-                  make_uint4(w[kh][rb][0], w[kh][rb][1], w[kh][rb][2], w[kh][rb][3]);
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          scaled_parity[stage] = static_cast<int>(phase);
-          mbar_arrive(&full_bar[stage]);
+        for (int i = 0; i < 4; ++i) {                                // [A0 kh0][A0 kh1][A1 kh0][A1 kh1]
+          const uint4 y = sf[32 * i];
+          w[4 * i] = y.x; w[4 * i + 1] = y.y; w[4 * i + 2] = y.z; w[4 * i + 3] = y.w;
         }
-        if (kb + 1 < nk) fetch(kb + 1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[16 + i] = x[i];
+        tc_fence_after();
+        tmem_st32(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + 2 * bn + 32u * stage, w);
+        if (kb + 1 < nk) fetch(kb + 1);                              // in flight while the store completes
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&scaled_bar[stage]);
         if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
     }
@@ -375,29 +390,26 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, it = 0;
+      const uint64_t ad0 = sw128_desc(smem_u32(sA(0))), bd0 = sw128_desc(smem_u32(sB(0)));
       int g = 0;
       for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x, ++it) {
         const SegTile ti = decode_tile(sched, sp, t, g);
         const uint32_t id0 = mxf4_idesc(128u, static_cast<uint32_t>(ti.N), 0u);
         const uint32_t id1 = mxf4_idesc(128u, static_cast<uint32_t>(ti.N), 1u);
-        const bool wide = ti.N > 128;
         if (!mbar_wait(&tmem_empty, (it & 1u) ^ 1u, &abort_flag, a.status, a.wait_ns)) break;
         tc_fence_after();
         bool ok = true;
         uint32_t acc = 0;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait(&full_bar[stage], phase, &abort_flag, a.status, a.wait_ns)) { ok = false; break; }
-          tc_fence_after();
-          const int halves = min(2, k128 - 2 * kb);
-          const uint32_t sf = tmem_base + 2 * bn + 32u * stage;      // [A0: 8][A1: 8][B: 16] columns
-          const uint32_t s_a = smem_u32(sSfa(stage)), s_b = smem_u32(sSfb(stage));
-          const uint64_t ad = sw128_desc(smem_u32(sA(stage))), bd = sw128_desc(smem_u32(sB(stage)));
-          for (int kh = 0; kh < halves; ++kh) {
-            tmem_copy_scales(sf + kh * 4, s_a + kh * 512);
-            tmem_copy_scales(sf + 8 + kh * 4, s_a + 1024 + kh * 512);
-            tmem_copy_scales(sf + 16 + kh * 8, s_b + kh * 1024);
-            if (wide) tmem_copy_scales(sf + 16 + kh * 8 + 4, s_b + kh * 1024 + 512);
+          if (!mbar_wait(&full_bar[stage], phase, &abort_flag, a.status, a.wait_ns) ||
+              !mbar_wait(&scaled_bar[stage], phase, &abort_flag, a.status, a.wait_ns)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+          const uint32_t sf = tmem_base + 2 * bn + 32u * stage;      // [A0: 8][A1: 8][B: 16] columns
+          const uint64_t ad = ad0 + stage * (stage_bytes >> 4), bd = bd0 + stage * (stage_bytes >> 4);
+          const int halves = min(2, k128 - 2 * kb);
           for (int kh = 0; kh < halves; ++kh) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {                            // 64 values: 32 B, 2 descriptor units
@@ -417,12 +429,12 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       umma_commit(&drain_bar);   // all issued MMAs must finish before TMEM is released
       mbar_wait_drain(&drain_bar, 0);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     const int q = warp & 3;
-    const int c0 = (warp - 4) / 4;
+    const int c0 = (warp - 8) / 4;
     constexpr int cstep = kMxEpi / 4;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-    float* ts = tile_s[warp - 4];
+    float* ts = tile_s[warp - 8];
     uint32_t it = 0;
     int g = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
@@ -469,18 +481,22 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       } else {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
         __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(ts);
-#pragma unroll 1
-        for (int s = 0; s < 2; ++s) {
-          for (int c = c0; c < nchunk; c += cstep) {
-            const int r = c * 32 + lane;
-            const float wl = a.row_w && r < ti.n_valid ? __ldg(a.row_w + ti.row0 + r) : 1.0f;
-            float v[32];
-            tmem_ld32(lane_addr + s * bn + c * 32, v);
-            tmem_ld_wait();
+        for (int c = c0; c < nchunk; c += cstep) {
+          const int row0 = ti.row0 + c * 32, n_rows = ti.n_valid - c * 32;
+          float w[8];
+          frag_row_values(a.row_w ? a.row_w + row0 : nullptr, n_rows, lane, 1.0f, w);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= __shfl_sync(0xffffffffu, wl, j);
-            store_tile<32>(stg, v, lane, out, static_cast<size_t>(a.out_ld), ti.row0 + c * 32, ti.n_valid - c * 32,
-                           ti.mb * 256 + s * 128 + 32 * q);
+          for (int s = 0; s < 2; ++s) {
+            float v[32];
+            tmem_ld_frag(lane_addr + s * bn + c * 32, v);
+            tmem_ld_wait();
+            uint32_t p[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int i = (k >> 1) & 3;
+              p[k] = pack_bf16(v[2 * k] * w[2 * i], v[2 * k + 1] * w[2 * i + 1]);
+            }
+            store_frag(stg, p, lane, out, static_cast<size_t>(a.out_ld), row0, n_rows, ti.mb * 256 + s * 128 + 32 * q);
           }
         }
       }
@@ -492,12 +508,10 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // after an abort every copy issued lands before the CTA leaves; where warp 2
-  // has not arrived on the stage, this thread does
-  if (abort_flag && warp == 0 && lane == 0) {
+  if (abort_flag && warp == 0 && lane == 0) {                        // every copy issued lands before the CTA leaves
     for (int i = 0; i < kMxMaxStages; ++i) {
       if (issued_parity[i] < 0) continue;
-      if (scaled_parity[i] != issued_parity[i]) mbar_arrive(&full_bar[i]);
+      mbar_wait_drain(&sfa_bar[i], static_cast<uint32_t>(issued_parity[i]));
       mbar_wait_drain(&full_bar[i], static_cast<uint32_t>(issued_parity[i]));
     }
   }

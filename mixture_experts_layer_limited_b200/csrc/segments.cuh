@@ -158,26 +158,104 @@ __device__ __forceinline__ int load_token_rows(int rows, LoadFn&& load) {
   return off;
 }
 
-// Writes NT tokens x 32 features (thread = feature lane, v[j] = token j) to
-// out[(row0 + j) * ld + feat0 + lane] through a per-warp shared tile, so that
-// every global store is a 16-byte vector (4 lanes cover one token's 32
-// features). Tokens j >= n_rows are not written.
-template <int NT>
-__device__ __forceinline__ void store_tile(__nv_bfloat16* stage, const float (&v)[NT], int lane,
-                                           __nv_bfloat16* out, size_t ld, int row0, int n_rows, int feat0) {
+// ---- 32 features x 32 rows of an accumulator, as the tensor cores' fragments
+// A warp's 32 TMEM lanes (features) x 32 columns (rows of the output): thread t
+// holds, in v[16 h + 4 i + 2 s + e], feature 16 h + 8 s + t / 4 of row
+// 8 i + 2 (t % 4) + e. Two rows (e) packed to bf16 are what stmatrix and ldmatrix
+// take, which transpose 8 x 8 blocks on the way, so that the output's rows, whose
+// features are contiguous, go through shared memory in 16-byte pieces (with one
+// feature per thread they would go in 2-byte ones, eight times as many).
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j) stage[j * 32 + lane] = __float2bfloat16_rn(v[j]);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16))
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[16 * h + i] = __uint_as_float(r[i]);
+  }
+}
+// The row of v[16 h + 4 i + 2 s + e] for thread t.
+__device__ __forceinline__ int frag_row(int lane, int i, int e) { return 8 * i + 2 * (lane & 3) + e; }
+
+// Packed fragments: p[8 h + 2 i + s] holds the rows e = 0 (low half) and 1.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void pack_frag(const float (&v)[32], uint32_t (&p)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) p[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+}
+// Byte offset of 16-byte piece `seg` (8 features) of row r in the warp's 2 KB tile.
+__device__ __forceinline__ uint32_t tile_piece(int r, int seg) {
+  return static_cast<uint32_t>(r * 64 + ((seg ^ ((r >> 1) & 3)) << 4));
+}
+// Stores packed fragments as rows [row0, +n_rows) x 32 features from feat0.
+__device__ __forceinline__ void store_frag(__nv_bfloat16* tile, const uint32_t (&p)[16], int lane, __nv_bfloat16* out,
+                                           size_t ld, int row0, int n_rows, int feat0) {
+  const uint32_t base = smem_u32(tile);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     base + tile_piece(8 * i + (lane & 7), lane >> 3)),
+                 "r"(p[2 * i]), "r"(p[2 * i + 1]), "r"(p[8 + 2 * i]), "r"(p[8 + 2 * i + 1])
+                 : "memory");
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < NT / 8; ++i) {
-    const int t = (lane >> 2) + 8 * i;
-    const int seg = lane & 3;
-    if (t < n_rows) {
-      const uint4 val = *reinterpret_cast<const uint4*>(stage + t * 32 + seg * 8);
-      *reinterpret_cast<uint4*>(out + static_cast<size_t>(row0 + t) * ld + feat0 + seg * 8) = val;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int r = (lane >> 2) + 8 * i, seg = lane & 3;
+    if (r < n_rows)
+      *reinterpret_cast<uint4*>(out + static_cast<size_t>(row0 + r) * ld + feat0 + seg * 8) =
+          *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(tile) + tile_piece(r, seg));
   }
   __syncwarp();
+}
+
+// 32 rows x 32 features of a bf16 matrix: fetched (rows >= n_rows as zeros) ..
+struct TileRegs { uint4 r[4]; };
+__device__ __forceinline__ TileRegs load_tile_regs(const __nv_bfloat16* src, size_t ld, int row0, int n_rows, int feat0,
+                                                   int lane) {
+  TileRegs t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (lane >> 2) + 8 * i;
+    t.r[i] = r < n_rows ? *reinterpret_cast<const uint4*>(src + static_cast<size_t>(row0 + r) * ld + feat0 + (lane & 3) * 8)
+                        : make_uint4(0u, 0u, 0u, 0u);
+  }
+  return t;
+}
+// .. and turned into packed fragments through the warp's tile.
+__device__ __forceinline__ void spread_frag(__nv_bfloat16* tile, const TileRegs& t, int lane, uint32_t (&p)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(tile) + tile_piece((lane >> 2) + 8 * i, lane & 3)) = t.r[i];
+  __syncwarp();
+  const uint32_t base = smem_u32(tile);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(p[2 * i]), "=r"(p[2 * i + 1]), "=r"(p[8 + 2 * i]), "=r"(p[8 + 2 * i + 1])
+                 : "r"(base + tile_piece(8 * i + (lane & 7), lane >> 3))
+                 : "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t p) {
+  return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
+}
+// The eight rows' values of a per-row vector that thread t's fragments need:
+// w[2 i + e], 0 for rows >= n_rows; nullptr: `none`.
+__device__ __forceinline__ void frag_row_values(const float* src, int n_rows, int lane, float none, float (&w)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = frag_row(lane, k >> 1, k & 1);
+    w[k] = r < n_rows ? (src ? __ldg(src + r) : none) : 0.0f;
+  }
 }
 
 // mbar_wait for a whole warp: one lane waits, so that all lanes go on, or give

@@ -149,46 +149,6 @@ __device__ void pair_drain(uint64_t* full, const uint32_t* loads, const uint32_t
 // ========================================================================
 // Products of a segment's rows with a weight
 // ========================================================================
-// Sums v[j] (j = 0..31, one value per lane each) over the warp's lanes; lane j
-// receives the sum of v[j]. Halving exchange: 31 shuffles instead of 160.
-__device__ __forceinline__ float lane_sums(float (&v)[32], int lane) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const bool up = (lane & d) != 0;
-#pragma unroll
-    for (int j = 0; j < d; ++j) {
-      const float send = up ? v[j] : v[j + d];
-      const float keep = up ? v[j + d] : v[j];
-      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, d);
-    }
-  }
-  return v[0];
-}
-
-// 32 rows x 32 features of a bf16 matrix through the warp's shared tile:
-// v[j] = row j's value of this lane's feature (0 for rows >= n_rows).
-struct TileRegs { uint4 r[4]; };
-__device__ __forceinline__ TileRegs load_tile_regs(const __nv_bfloat16* src, size_t ld, int row0, int n_rows, int feat0,
-                                                   int lane) {
-  TileRegs t;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (lane >> 2) + 8 * i;
-    t.r[i] = r < n_rows ? *reinterpret_cast<const uint4*>(src + static_cast<size_t>(row0 + r) * ld + feat0 + (lane & 3) * 8)
-                        : make_uint4(0u, 0u, 0u, 0u);
-  }
-  return t;
-}
-__device__ __forceinline__ void spread_tile(__nv_bfloat16* stage, const TileRegs& t, int lane, float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint4*>(stage + ((lane >> 2) + 8 * i) * 32 + (lane & 3) * 8) = t.r[i];
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = __bfloat162float(stage[j * 32 + lane]);
-  __syncwarp();
-}
-
 // SiLU's sigmoid with the fast exponential and division (relative error about
 // 2^-21, below that of the tensor cores' fp32 sums it multiplies).
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
@@ -209,8 +169,8 @@ __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f
 // 233 / 317 us.
 //   forward: sub-tile 0 holds the gate rows of the CTA's 128 features, sub-tile
 //   1 their up rows, so that one thread has both.
-// Warp 0 loads, warp 1 of the first CTA issues the MMAs, eight epilogue warps:
-// warp w reads TMEM lanes 32 (w % 4).. and every second 32-row chunk.
+// Warp 0 loads, warp 1 of the first CTA issues the MMAs, twelve epilogue warps:
+// warp w reads TMEM lanes 32 (w % 4).. and every third 32-row chunk.
 template <int MODE, int SUBS>
 struct PairCfg {
   static constexpr int KB = 64;
@@ -220,7 +180,7 @@ struct PairCfg {
   static constexpr uint32_t STAGE_BYTES = A_BYTES + 128 * 128;
   static constexpr int ACCS = SUBS == 2 ? 1 : 2;
   static constexpr int FEATS = MODE == TRAIN_FORWARD ? 256 : SUBS * 256;   // features per tile, half of them per CTA
-  static constexpr int EPIW = 8;
+  static constexpr int EPIW = 12;
   static constexpr int THREADS = 64 + 32 * EPIW;
 };
 template <int MODE, int SUBS>
@@ -408,60 +368,90 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
           const int row0 = ti.row0 + c * 32, n_rows = ti.n_valid - c * 32;
           const int row1 = row0 + 32 * cstep, n_rows1 = n_rows - 32 * cstep;   // the next chunk's
           float v[32];
-          tmem_ld32(acc + c * 32, v);
+          uint32_t p[16];
+          tmem_ld_frag(acc + c * 32, v);
           if (MODE == TRAIN_FORWARD) {
             // h from the fp32 sums; the pre-activations are rounded once, for the backward pass
             float u[32];
-            tmem_ld32(acc + 256 + c * 32, u);
+            tmem_ld_frag(acc + 256 + c * 32, u);
             tmem_ld_wait();
-            store_tile<32>(stg, v, lane, a.gu, ld, row0, n_rows, feat0);
-            store_tile<32>(stg, u, lane, a.gu, ld, row0, n_rows, a.M + feat0);
+            pack_frag(v, p);
+            store_frag(stg, p, lane, a.gu, ld, row0, n_rows, feat0);
+            pack_frag(u, p);
+            store_frag(stg, p, lane, a.gu, ld, row0, n_rows, a.M + feat0);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = silu(v[j]) * u[j];
-            store_tile<32>(stg, v, lane, a.h, static_cast<size_t>(a.M), row0, n_rows, feat0);
+            pack_frag(v, p);
+            store_frag(stg, p, lane, a.h, static_cast<size_t>(a.M), row0, n_rows, feat0);
           } else if (MODE == TRAIN_HIDDEN) {
-            tmem_ld_wait();
-            const float w = lane < n_rows ? (a.row_w ? __ldg(a.row_w + row0 + lane) : 1.0f) : 0.0f;
-            float g[32], u[32], hw[32];
-            spread_tile(stg, gr, lane, g);
-            spread_tile(stg, ur, lane, u);
+            float w[8];
+            frag_row_values(a.row_w ? a.row_w + row0 : nullptr, n_rows, lane, 1.0f, w);
+            uint32_t g[16], u[16];
+            spread_frag(stg, gr, lane, g);
+            spread_frag(stg, ur, lane, u);
             if (c + cstep < nchunk) {                              // the next chunk's, while this one is computed
               gr = load_tile_regs(a.gu, ld, row1, n_rows1, feat0, lane);
               ur = load_tile_regs(a.gu, ld, row1, n_rows1, a.M + feat0, lane);
             }
-            // g <- dg, u <- du, v <- h dh0, hw = row_w h
+            tmem_ld_wait();
+            // g <- dg, u <- du, p <- row_w h; sums of h dh0 over this thread's four features of each row
+            float sum[8];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float wj = __shfl_sync(0xffffffffu, w, j);
-              const float sg = sigmoid(g[j]);
-              const float act = g[j] * sg;                         // SiLU(g)
-              const float dh = v[j] * wj;
-              const float h = act * u[j];
-              v[j] *= h;
-              hw[j] = h * wj;
-              const float dg = dh * u[j] * sg * fmaf(g[j], 1.0f - sg, 1.0f);
-              u[j] = dh * act;
-              g[j] = dg;
+            for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int i = (k >> 1) & 3;
+              const float2 gk = unpack_bf16(g[k]), uk = unpack_bf16(u[k]);
+              float dg[2], du[2], hw[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float ge = e ? gk.y : gk.x, ue = e ? uk.y : uk.x, we = w[2 * i + e], dh0 = v[2 * k + e];
+                const float sg = sigmoid(ge);
+                const float act = ge * sg;                         // SiLU(g)
+                const float dh = dh0 * we, h = act * ue;
+                sum[2 * i + e] = fmaf(h, dh0, sum[2 * i + e]);
+                hw[e] = h * we;
+                dg[e] = dh * ue * sg * fmaf(ge, 1.0f - sg, 1.0f);
+                du[e] = dh * act;
+              }
+              g[k] = pack_bf16(dg[0], dg[1]);
+              u[k] = pack_bf16(du[0], du[1]);
+              p[k] = pack_bf16(hw[0], hw[1]);
             }
-            store_tile<32>(stg, g, lane, a.d_gu, ld, row0, n_rows, feat0);
-            store_tile<32>(stg, u, lane, a.d_gu, ld, row0, n_rows, a.M + feat0);
-            store_tile<32>(stg, hw, lane, a.h, static_cast<size_t>(a.M), row0, n_rows, feat0);
-            const float part = lane_sums(v, lane);
-            if (lane < n_rows) a.partial[static_cast<size_t>(feat0 / 32) * a.rows + row0 + lane] = part;
+            store_frag(stg, g, lane, a.d_gu, ld, row0, n_rows, feat0);
+            store_frag(stg, u, lane, a.d_gu, ld, row0, n_rows, a.M + feat0);
+            store_frag(stg, p, lane, a.h, static_cast<size_t>(a.M), row0, n_rows, feat0);
+            // over the 8 lanes t / 4 that hold the other features: lane t is left with sum t / 4's row
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) {
+              const bool up = ((lane >> 2) & d) != 0;
+#pragma unroll
+              for (int k = 0; k < d; ++k) {
+                const float send = up ? sum[k] : sum[k + d], keep = up ? sum[k + d] : sum[k];
+                sum[k] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * d);
+              }
+            }
+            const int r = frag_row(lane, lane >> 3, (lane >> 2) & 1);
+            if (r < n_rows) a.partial[static_cast<size_t>(feat0 / 32) * a.rows + row0 + r] = sum[0];
           } else {
             tmem_ld_wait();
             if (a.add) {
-              float add[32];
-              spread_tile(stg, gr, lane, add);
+              uint32_t add[16];
+              spread_frag(stg, gr, lane, add);
               if (c + cstep < nchunk)
                 gr = load_tile_regs(a.add, static_cast<size_t>(a.M), row1, n_rows1, feat0, lane);
               else if (s + 1 < PASSES && feat0 + 128 < a.M)
                 gr = load_tile_regs(a.add, static_cast<size_t>(a.M), ti.row0 + c0 * 32, ti.n_valid - c0 * 32, feat0 + 128,
                                     lane);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += add[j];
+              for (int k = 0; k < 16; ++k) {
+                const float2 o = unpack_bf16(add[k]);
+                v[2 * k] += o.x;
+                v[2 * k + 1] += o.y;
+              }
             }
-            store_tile<32>(stg, v, lane, a.out, static_cast<size_t>(a.M), row0, n_rows, feat0);
+            pack_frag(v, p);
+            store_frag(stg, p, lane, a.out, static_cast<size_t>(a.M), row0, n_rows, feat0);
           }
         }
       }
