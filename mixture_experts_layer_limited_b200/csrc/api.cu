@@ -916,7 +916,8 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
   g.status = dev_status;
   g.wait_ns = wait_limit();
   if ((s = check_launch(launch_train_gemm(TRAIN_HIDDEN, 1, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
-  if (d_row_w) {
+  const bool weights = d_w13 || d_w2;
+  if (d_row_w && !weights) {                           // else with the weight gradients
     s = check_launch(launch_row_w_grad(rows, I / 32, partial, offsets, w->groups, d_row_w, st));
     if (s != MOE_OK) return s;
   }
@@ -930,7 +931,7 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
     g.out = static_cast<__nv_bfloat16*>(d_a);
     if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, subs, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
   }
-  if (d_w13 || d_w2) {
+  if (weights) {
     WgradArgs q{};
     const bool f32 = grad_dtype == MOE_F32;
     if (d_w13) {
@@ -946,6 +947,10 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
     q.offsets = offsets;
     q.f32 = f32;
     q.accumulate = accumulate;
+    q.after = d_a ? 1 : 0;
+    q.partial = partial;
+    q.d_row_w = d_row_w;
+    q.n_partial = I / 32;
     q.status = dev_status;
     q.wait_ns = wait_limit();
     s = check_launch(launch_wgrad(q, nsm, st));
@@ -1003,6 +1008,7 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
     q.groups = 1;
     q.f32 = grad_dtype == MOE_F32;
     q.accumulate = accumulate;
+    q.after = dx ? 1 : 0;
     q.status = dev_status;
     q.wait_ns = wait_limit();
     s = check_launch(launch_wgrad(q, nsm, st));

@@ -235,8 +235,8 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     for (int i = 0; i < 8; ++i) tma_prefetch_desc(&tmB.box[i]);
   }
   if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 512);
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();                                     // after the wait: see wgrad_kernel's `after`
   if (warp == 2) build_schedule(sm.sched, sp, lane);
   tc_fence_before();
   __syncthreads();
@@ -470,8 +470,15 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
 }
 
-// d_row_w[r] = sum of the row's partial sums, in feature order; rows outside
-// [offsets[0], offsets[groups]) are left as they were.
+// A row's d_row_w: its partial sums, in feature order.
+__device__ __forceinline__ float sum_partials(const float* __restrict__ partial, int n, int rows, int r) {
+  float s = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) s += partial[static_cast<size_t>(i) * rows + r];
+  return s;
+}
+// d_row_w where no weight gradients are asked for (else wgrad_kernel does it);
+// rows outside [offsets[0], offsets[groups]) are left as they were.
 __global__ void __launch_bounds__(256)
 row_w_grad_kernel(int rows, int n, const float* __restrict__ partial, const int32_t* __restrict__ offsets, int groups,
                   float* __restrict__ d_row_w) {
@@ -480,9 +487,7 @@ row_w_grad_kernel(int rows, int n, const float* __restrict__ partial, const int3
   const int r = blockIdx.x * 256 + threadIdx.x;
   const int lo = offsets ? offsets[0] : 0, hi = offsets ? offsets[groups] : rows;   // r < rows bounds both
   if (r >= rows || r < lo || r >= hi) return;
-  float s = 0.0f;
-  for (int i = 0; i < n; ++i) s += partial[static_cast<size_t>(i) * rows + r];
-  d_row_w[r] = s;
+  d_row_w[r] = sum_partials(partial, n, rows, r);
 }
 
 // ========================================================================
@@ -504,6 +509,11 @@ row_w_grad_kernel(int rows, int n, const float* __restrict__ partial, const int3
 // step are zeroed in both operands by a warp of their own (a neighbour's row may
 // hold anything, and 0 * NaN is NaN); that block's loads complete on a barrier of
 // each CTA's own.
+//
+// `after`: the kernel before this one in the stream is a train_gemm_kernel this
+// one does not depend on. It let this one start only after all before it had
+// completed, so this one runs beside it (on the SMs it leaves) and waits for its
+// end before its own.
 //
 // Measured on B200 at V3 widths, 32 experts: 256 rows each 777 us (3.6 TB/s
 // written, 930 TFLOP/s), 251 rows 792 us, 16 rows 470 us (6.0 TB/s written).
@@ -626,8 +636,10 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
     }
   }
   if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 512);
-  griddep_launch_dependents();
-  griddep_wait();
+  if (!a.after) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
   for (int i = threadIdx.x; i <= a.groups; i += blockDim.x)
     sm.off[i] = a.offsets ? min(max(a.offsets[i], 0), a.rows) : i * a.rows;
   tc_fence_before();
@@ -757,6 +769,13 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
   } else {
     const int q = warp & 3, half = (warp - 2) / 4;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    // d_row_w, while the first tile's products run: rows outside [offsets[0],
+    // offsets[groups]) are left as they were
+    if (a.d_row_w) {
+      const int hi = off[a.groups];
+      for (int r = off[0] + blockIdx.x * 32 * EPIW + threadIdx.x - 64; r < hi; r += gridDim.x * 32 * EPIW)
+        a.d_row_w[r] = sum_partials(a.partial, a.n_partial, a.rows, r);
+    }
     uint8_t* box = sm.out[warp - 2];                               // 32 rows x 128 B
     const int cols = a.f32 ? 32 : 64;                              // columns of such a row
     uint32_t it = 0;
@@ -832,6 +851,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
   cluster_sync();                                                  // nothing of either CTA is used any more
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+  if (a.after) griddep_wait();                                     // what follows this kernel follows that one too
 }
 
 // ========================================================================

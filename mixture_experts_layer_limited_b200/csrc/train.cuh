@@ -50,6 +50,10 @@ struct WgradArgs {
   int32_t n_prob, rows, groups;
   const int32_t* offsets;
   int32_t f32, accumulate;            // output type; fp32 only: add to what is there
+  int32_t after;                      // launched behind a train_gemm_kernel it does not depend on
+  const float* partial;               // also d_row_w from its partial sums [n_partial, rows], or
+  float* d_row_w;                     //   nullptr
+  int32_t n_partial;
   int32_t* status;
   uint64_t wait_ns;
 };
