@@ -292,6 +292,11 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
+      // the MMAs' last commits to this CTA's barriers have arrived before it leaves
+      for (int i = 0; i < STAGES && ok && !*abort_flag; ++i) {
+        ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, a.status, a.wait_ns);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
@@ -683,7 +688,12 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (*abort_flag)                                             // this CTA's tail loads; the others: below
+      // the MMAs' last commits to this CTA's barriers have arrived before it leaves
+      for (int i = 0; i < STAGES && ok && !*abort_flag; ++i) {
+        ok = mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, a.status, a.wait_ns);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+      if (*abort_flag)                                             // this CTA's tail loads; the others: pair_drain
         for (int i = 0; i < STAGES; ++i)
           if (sm.tails[i]) mbar_wait_drain(&sm.tail_full[i], (sm.tails[i] - 1) & 1u);
     }

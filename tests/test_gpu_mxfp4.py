@@ -229,3 +229,35 @@ def test_nan_scale_stays_in_its_row():
     N.moe_down_proj(R, H, X.pack(c["w2"]), N.MOE_MXFP4, E, I, X.pack(c["h"]), None, None, out,
                     w2_scale=X.weight_scale_blocks(c["w2s"]), h_scale=X.row_scale_words(hs))
     assert bool(torch.isnan(out[7]).all()) and bool(torch.isfinite(out[:7]).all()) and bool(torch.isfinite(out[8:]).all())
+
+
+def test_wait_limit_runs_out_then_the_same_call_is_correct():
+    """As for the bf16 products: a wait limit of a few nanoseconds ends the
+    kernels with MOE_DEVSTAT_TIMEOUT, and the same call is right afterwards."""
+    H, I = 768, 384
+    c, off, R, E = _layer([40, 0, 150, 3], H, I, seed=8)
+    offs = torch.tensor(off, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    u8 = dict(dtype=torch.uint8, device=DEV)
+    a, w13, w2 = X.pack(c["x"]), X.pack(c["w13"]), X.pack(c["w2"])
+    s = dict(w13_scale=X.weight_scale_blocks(c["w13s"]), w2_scale=X.weight_scale_blocks(c["w2s"]),
+             a_scale=X.row_scale_words(c["xs"]))
+
+    def run():
+        h, hs, out = torch.zeros(R, I // 2, **u8), torch.zeros(I // 128, R, 4, **u8), torch.zeros(R, H, dtype=BF, device=DEV)
+        N.moe_grouped_swiglu(R, H, w13, w2, N.MOE_MXFP4, E, I, a, offs, c["row_w"], h, out, h_scale_ws=hs,
+                             dev_status=status, **s)
+        return (h, hs, out), N.moe_read_device_status(status)
+    before, st = run()
+    assert st == 0
+    N.moe_set_wait_limit_ns(5)
+    try:
+        _, st = run()
+    finally:
+        N.moe_set_wait_limit_ns(0)
+    assert st == N.MOE_DEVSTAT_TIMEOUT
+    status.zero_()
+    after, st = run()
+    assert st == 0
+    for x, y in zip(before, after):
+        assert torch.equal(x, y)

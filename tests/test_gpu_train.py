@@ -300,3 +300,45 @@ def test_gate_backward(T, H, E):
     N.moe_gate_backward(T, H, E, dl, x, None, None, None, acc, grad_dtype=N.MOE_F32, accumulate=True)
     ref = L.T @ X
     assert bool(((acc.to(F64) - 1 - ref).abs() <= 2 * F32_U * (1 + ref.abs()) + T * F32_U * (L.abs().T @ X.abs())).all())
+
+
+# -------------------------------------------------- bounded waits time out
+@pytest.mark.parametrize("call", ["forward", "backward", "gate"])
+def test_wait_limit_runs_out_then_the_same_call_is_correct(call):
+    """With a wait limit of a few nanoseconds the kernels give up at the first
+    wait that does not succeed at once: they flag MOE_DEVSTAT_TIMEOUT, let
+    their copies and MMAs end, free their tensor memory and return. The same
+    call with the default limit then gives what it gave before."""
+    H, I, counts = 512, 384, [300, 17, 0, 129]
+    c, off, R, E = _case(counts, H, I, seed=31)
+    offs = torch.tensor(off, dtype=torch.int32, device=DEV)
+    g = _gen(32)
+    dl, gate = (torch.randn(R, 48, generator=g, device=DEV)).to(BF), torch.randn(48, H, generator=g, device=DEV).to(BF)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = torch.empty(N.moe_swiglu_ffn_backward_workspace_size(R, I), dtype=torch.uint8, device=DEV)
+
+    def run():
+        if call == "forward":
+            o = [torch.zeros(R, I, dtype=BF, device=DEV), torch.zeros(R, 2 * I, dtype=BF, device=DEV)]
+            N.moe_gate_up_swiglu_train(R, H, c["w13"], E, I, c["a"], offs, *o, dev_status=status)
+        elif call == "backward":
+            o = [torch.zeros_like(c["a"]), torch.zeros_like(c["w13"]), torch.zeros_like(c["w2"]), torch.zeros(R, device=DEV)]
+            N.moe_swiglu_ffn_backward(R, H, c["w13"], c["w2"], E, I, c["a"], c["gu"], c["d_out"], offs, c["row_w"], *o, ws,
+                                      dev_status=status)
+        else:
+            o = [torch.zeros_like(c["a"]), torch.zeros_like(gate)]
+            N.moe_gate_backward(R, H, 48, dl, c["a"], gate, None, *o, dev_status=status)
+        return o, N.moe_read_device_status(status)
+    before, st = run()
+    assert st == 0
+    N.moe_set_wait_limit_ns(5)
+    try:
+        _, st = run()
+    finally:
+        N.moe_set_wait_limit_ns(0)
+    assert st == N.MOE_DEVSTAT_TIMEOUT
+    status.zero_()
+    after, st = run()
+    assert st == 0
+    for a, b in zip(before, after):
+        assert torch.equal(a, b)
