@@ -136,7 +136,7 @@ class MoELayer:
             self.sh_h_s = z(T_max * max(I_s, 128) // 32, dt=torch.uint8)
         else:
             self.xq = self.xs = self.x_perm_s = self.h_s = self.sh_h_s = None
-        self._train = None                     # what forward_train keeps for backward
+        self._train = self._train_x = None     # forward_train()'s buffers, and its x until backward()
         if I_s > 0:
             self.sh_h = z(T_max, I_s // pack, dt=act)
             self.sh_o = z(T_max, H, dt=bf)
@@ -174,6 +174,7 @@ class MoELayer:
     # -------------------------------------------------------------- stages
     def route(self, x: torch.Tensor, write_logits: bool = False, logits_in: Optional[torch.Tensor] = None):
         s = self.spec
+        self._train_x = None                   # this routing replaces forward_train()'s
         T = (logits_in if logits_in is not None else x).shape[0]
         N.moe_route(T, s.H, s.E, s.k, s.n_group, s.topk_group,
                     N.MOE_SIGMOID if s.scoring == "sigmoid" else N.MOE_SOFTMAX,
@@ -377,7 +378,9 @@ class MoELayer:
     def forward_train(self, x: torch.Tensor) -> torch.Tensor:
         """forward() of a bf16 layer that keeps what backward() needs: x itself
         (not to be changed before it), the routing and the pre-activations, in
-        the layer's buffers: one backward() belongs to the last forward_train()."""
+        the layer's buffers. backward() belongs to the last forward_train(); a
+        forward() in between takes the buffers and ends that. Run the step once
+        before capturing it into a CUDA graph (the buffers are allocated then)."""
         s, T = self.spec, x.shape[0]
         if self.quant or self.gather:
             raise ValueError("forward_train needs a bf16 layer without gather")
@@ -412,7 +415,7 @@ class MoELayer:
         returned ([T, H] bf16, the layer's buffer). The selection bias, the
         groups and the choice of experts have no gradient."""
         s, t = self.spec, self._train
-        if t is None or getattr(self, "_train_x", None) is None:
+        if t is None or self._train_x is None:
             raise ValueError("backward() without forward_train()")
         x = self._train_x
         T, R = x.shape[0], x.shape[0] * s.k

@@ -102,6 +102,59 @@ def test_backward_leaves_rows_of_nobody_alone():
     _check(_backward(c, off, R, E, 256, 128), c, off, 256, 128)
 
 
+def test_backward_without_any_row():
+    """No expert has a row: the weights' gradients are zero (left alone when
+    accumulating), nothing else is written."""
+    H, I = 256, 128
+    c, off, R, E = _case([0, 0, 0], H, I, seed=14, lead=1, behind=2)
+    o = _backward(c, off, R, E, H, I)
+    assert bool((o["d_w13"] == 0).all()) and bool((o["d_w2"] == 0).all())
+    assert bool((o["d_a"] == 7).all()) and bool((o["d_row_w"] == 7).all())
+    init = (torch.full((E, 2 * I, H), 3.0, device=DEV), torch.full((E, H, I), 4.0, device=DEV))
+    o = _backward(c, off, R, E, H, I, f32=True, accumulate=True, init=init)
+    assert bool((o["d_w13"] == 3).all()) and bool((o["d_w2"] == 4).all())
+
+
+def test_segments_outside_the_rows_are_cut_and_flagged():
+    """offsets past the rows there are: nothing is read or written outside."""
+    H, I = 256, 128
+    c, off, R, E = _case([20, 30], H, I, seed=15)
+    good = _backward(c, off, R, E, H, I)
+    offs = torch.tensor([0, 20, 10_000], dtype=torch.int32, device=DEV)
+    o = {k: torch.zeros_like(v) for k, v in good.items()}
+    ws = torch.empty(N.moe_swiglu_ffn_backward_workspace_size(R, I), dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    N.moe_swiglu_ffn_backward(R, H, c["w13"], c["w2"], E, I, c["a"], c["gu"], c["d_out"], offs, c["row_w"], o["d_a"],
+                              o["d_w13"], o["d_w2"], o["d_row_w"], ws, dev_status=status)
+    assert N.moe_read_device_status(status) & N.MOE_DEVSTAT_BAD_EXPERT_ID
+    for k in good:
+        assert torch.equal(o[k], good[k])
+
+
+def test_calls_on_two_streams_at_once():
+    """Two backward passes in flight at once, a workspace each, give what they
+    give one after the other."""
+    H, I = 512, 384
+    cases = [_case([90, 7, 0, 200], H, I, seed=s) for s in (16, 17)]
+    want = [_backward(c, off, R, E, H, I) for c, off, R, E in cases]
+    got, streams = [], [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s, (c, off, R, E) in zip(streams, cases):
+            with torch.cuda.stream(s):
+                o = {k: torch.zeros_like(v) for k, v in want[0].items()}
+                ws = torch.empty(N.moe_swiglu_ffn_backward_workspace_size(R, I), dtype=torch.uint8, device=DEV)
+                offs = torch.tensor(off, dtype=torch.int32, device=DEV)
+                N.moe_swiglu_ffn_backward(R, H, c["w13"], c["w2"], E, I, c["a"], c["gu"], c["d_out"], offs, c["row_w"],
+                                          o["d_a"], o["d_w13"], o["d_w2"], o["d_row_w"], ws)
+                got.append((o, ws, offs))
+        torch.cuda.synchronize()
+    for (o, _, _), w in zip(got, want):
+        for k in w:
+            assert torch.equal(o[k], w[k])
+
+
 def test_backward_nan_in_one_expert_stays_there():
     """The rows behind a segment's end are the next expert's: NaN and infinity
     in them must not reach this expert's weight gradients."""
@@ -228,6 +281,21 @@ def test_forward_backward_against_differences():
 
 
 # ------------------------------------------------------------------ router
+def test_python_checks_sizes_types_and_layout():
+    H, I = 256, 128
+    c, off, R, E = _case([20, 30], H, I, seed=18)
+    offs = torch.tensor(off, dtype=torch.int32, device=DEV)
+    h, gu = torch.empty(R, I, dtype=BF, device=DEV), torch.empty(R, 2 * I, dtype=BF, device=DEV)
+    call = lambda **kw: N.moe_gate_up_swiglu_train(*[{**dict(rows=R, H=H, w13=c["w13"], groups=E, I=I, a=c["a"], offsets=offs,
+                                                            h=h, gu=gu), **kw}[k]
+                                                     for k in ("rows", "H", "w13", "groups", "I", "a", "offsets", "h", "gu")])
+    call()
+    for bad in (dict(gu=gu[:-1]), dict(h=h.float()), dict(a=c["a"].cpu()), dict(offsets=offs.long()),
+                dict(a=c["a"].t().contiguous().t())):
+        with pytest.raises(ValueError):
+            call(**bad)
+
+
 ROUTES = [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)]
 
 

@@ -128,6 +128,10 @@ def test_training_refusals():
     with pytest.raises(ValueError):
         layer.backward(inp.x, layer.grad_buffers())      # no forward_train
     layer.forward_train(inp.x)
+    layer.forward(inp.x)
+    with pytest.raises(ValueError):
+        layer.backward(inp.x, layer.grad_buffers())      # a forward() took its buffers
+    layer.forward_train(inp.x)
     with pytest.raises(ValueError):
         layer.backward(inp.x[:3], layer.grad_buffers())
     with pytest.raises(ValueError):
@@ -167,6 +171,19 @@ def test_mxfp4_layer(name):
     assert _norm_err(y, ref) <= 2 * BF16_U + 0.34 * 1e-3 ** 0.5
     again = layer.forward(x)
     assert torch.equal(y, again)
+
+
+def test_mxfp4_layer_through_the_host_pipeline():
+    from mixture_experts_layer_limited_b200 import HostPipeline
+    cfg = dataclasses.replace(_cfg("wide"), dtype="mxfp4")
+    inp, layer = _layer(cfg)
+    xs = [(inp.x * s).cpu().pin_memory() for s in (1.0, -2.0, 0.5)]
+    want = [layer.forward(x.to(DEV)).cpu().clone() for x in xs]
+    ys = [torch.empty_like(x).pin_memory() for x in xs]
+    HostPipeline(layer, cfg.T).run(xs, ys)
+    torch.cuda.synchronize()
+    for y, w in zip(ys, want):
+        assert torch.equal(y, w)
 
 
 def test_mxfp4_layer_captured():

@@ -165,7 +165,7 @@ def test_route_formula_against_differences(scoring, norm):
     g, = torch.autograd.grad(f(x), x)
     d, eps = torch.randn_like(x), 1e-6
     diff = (f(x + eps * d) - f(x - eps * d)) / (2 * eps)
-    assert float((g * d).sum()) == pytest.approx(float(diff), rel=1e-6, abs=1e-8)
+    assert float((g * d).sum()) == pytest.approx(float(diff.detach()), rel=1e-6, abs=1e-8)
 
 
 def test_mx_definition_on_known_blocks():
