@@ -855,6 +855,8 @@ moe_status plan_wgrad(WgradProblem* p, int32_t rows, int32_t groups, const void*
   return MOE_OK;
 }
 
+int tiles_in_int(long long tiles) { return tiles < (1 << 20) ? static_cast<int>(tiles) : 1 << 20; }
+
 bool grad_args_ok(moe_dtype grad_dtype, int32_t accumulate) {
   if (grad_dtype != MOE_BF16 && grad_dtype != MOE_F32) return false;
   return accumulate == 0 || (accumulate == 1 && grad_dtype == MOE_F32);
@@ -917,18 +919,20 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
   g.wait_ns = wait_limit();
   if ((s = check_launch(launch_train_gemm(TRAIN_HIDDEN, 1, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
   const bool weights = d_w13 || d_w2;
+  int rows_tiles = 0;                                  // of the kernel the weight gradients run beside
   if (d_row_w && !weights) {                           // else with the weight gradients
     s = check_launch(launch_row_w_grad(rows, I / 32, partial, offsets, w->groups, d_row_w, st));
     if (s != MOE_OK) return s;
   }
   if (d_a) {                                           // d_a = d_gu w13
-    const int subs = train_subs(TRAIN_ROWS, 2 * I);
+    const int subs = train_subs(rows, w->groups, 2 * I, H, nsm);
     s = make_train_weight_tmap(&tmA, w->w13, TRAIN_ROWS, w->tiled, w->groups, 2 * I, H, subs);
     if (s != MOE_OK) return s;
     if ((s = make_half_tmaps(&tmB, d_gu, 2 * static_cast<uint64_t>(I), rows)) != MOE_OK) return s;
     g.K = 2 * I;
     g.M = H;
     g.out = static_cast<__nv_bfloat16*>(d_a);
+    rows_tiles = tiles_in_int(train_tiles(rows, w->groups, H, subs * 256));
     if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, subs, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
   }
   if (weights) {
@@ -948,6 +952,7 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
     q.f32 = f32;
     q.accumulate = accumulate;
     q.after = d_a ? 1 : 0;
+    q.beside = rows_tiles;
     q.partial = partial;
     q.d_row_w = d_row_w;
     q.n_partial = I / 32;
@@ -984,10 +989,11 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
   moe_status s = sm_count(&nsm);
   if (s != MOE_OK) return s;
   cudaStream_t st = as_stream(stream);
+  int rows_tiles = 0;
   if (dx) {                                            // dx = dx_in + d_logits gate
     CUtensorMap tmA;
     HalfMaps tmB;
-    const int subs = train_subs(TRAIN_ROWS, E);
+    const int subs = train_subs(T, 1, E, H, nsm);
     if ((s = make_train_weight_tmap(&tmA, gate_w, TRAIN_ROWS, 0, 1, E, H, subs)) != MOE_OK) return s;
     if ((s = make_half_tmaps(&tmB, d_logits_bf16, E, T)) != MOE_OK) return s;
     TrainGemmArgs g;
@@ -996,6 +1002,7 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
     g.M = H;
     g.out = static_cast<__nv_bfloat16*>(dx);
     g.add = static_cast<const __nv_bfloat16*>(dx_in);
+    rows_tiles = tiles_in_int(train_tiles(T, 1, H, subs * 256));
     g.status = dev_status;
     g.wait_ns = wait_limit();
     if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, subs, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
@@ -1009,6 +1016,7 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
     q.f32 = grad_dtype == MOE_F32;
     q.accumulate = accumulate;
     q.after = dx ? 1 : 0;
+    q.beside = rows_tiles;
     q.status = dev_status;
     q.wait_ns = wait_limit();
     s = check_launch(launch_wgrad(q, nsm, st));

@@ -969,8 +969,7 @@ static cudaError_t train_gemm(const CUtensorMap& tmA, const HalfMaps& tmB, Train
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   a.n_mblk = (a.M + C::FEATS - 1) / C::FEATS;
-  // tiles at most: each non-empty segment adds at most one partial row block
-  const long long most = (static_cast<long long>(a.rows + 255) / 256 + a.groups) * a.n_mblk;
+  const long long most = train_tiles(a.rows, a.groups, a.M, C::FEATS);
   const int pairs = num_sms / 2 < most ? num_sms / 2 : static_cast<int>(most);
   return launch_after(train_gemm_kernel<MODE, SUBS>, 2 * pairs, C::THREADS, smem, stream, tmA, tmB, a);
 }
@@ -1000,7 +999,10 @@ cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int tiles = a.prob[0].tiles + (a.n_prob > 1 ? a.prob[1].tiles : 0);
-  const int pairs = num_sms / 2 < tiles ? num_sms / 2 : tiles;
+  // where the kernel before leaves most SMs idle, this one takes those alone: a
+  // pair that had to wait for that one's end would do its share of the tiles late
+  const int all = num_sms / 2, room = a.after && 2 * a.beside <= all ? all - a.beside : all;
+  const int pairs = room < tiles ? room : tiles;
   return launch_after(wgrad_kernel, 2 * pairs, WgradCfg::THREADS, smem, stream, a);
 }
 

@@ -29,8 +29,17 @@ struct TrainGemmArgs {
 struct HalfMaps {
   CUtensorMap box[8];
 };
-// Sub-tiles per CTA of a product of K terms (see train_gemm_kernel).
-inline int train_subs(int mode, int K) { return mode == TRAIN_FORWARD || (mode == TRAIN_ROWS && K > 512) ? 2 : 1; }
+// Tiles of `feats` features x 256 rows at most: each segment that has rows adds
+// at most one partial row block.
+inline long long train_tiles(int rows, int groups, int M, int feats) {
+  return (static_cast<long long>(rows) / 256 + (groups < rows ? groups : rows)) * ((M + feats - 1) / feats);
+}
+// Sub-tiles per CTA of a TRAIN_ROWS product of K terms (see train_gemm_kernel):
+// two for a long K, where that leaves a tile for each pair of SMs. (48 rows on 8
+// experts, K = 1280, 768 features: 16 tiles of 512 features, 13.6 us.)
+inline int train_subs(int rows, int groups, int K, int M, int num_sms) {
+  return K > 512 && train_tiles(rows, groups, M, 512) >= num_sms / 2 ? 2 : 1;
+}
 cudaError_t launch_train_gemm(int mode, int subs, const CUtensorMap& tmA, const HalfMaps& tmB, const TrainGemmArgs& a,
                               int num_sms, cudaStream_t stream);
 cudaError_t launch_row_w_grad(int rows, int n, const float* partial, const int32_t* offsets, int groups, float* d_row_w,
@@ -50,7 +59,7 @@ struct WgradArgs {
   int32_t n_prob, rows, groups;
   const int32_t* offsets;
   int32_t f32, accumulate;            // output type; fp32 only: add to what is there
-  int32_t after;                      // launched behind a train_gemm_kernel it does not depend on
+  int32_t after, beside;              // launched behind a train_gemm_kernel it does not depend on, of so many tiles
   const float* partial;               // also d_row_w from its partial sums [n_partial, rows], or
   float* d_row_w;                     //   nullptr
   int32_t n_partial;

@@ -136,7 +136,7 @@ def _ptr(t: Optional[torch.Tensor]):
         raise ValueError("libmoe takes device tensors")
     if not t.is_contiguous():
         raise ValueError("libmoe takes contiguous tensors")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 # The current stream's handle of a device; torch.cuda.current_stream() builds a
@@ -146,9 +146,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(stream=None):
     if stream is None and _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
 def _check(fn: str, status: int):
@@ -169,13 +168,14 @@ def _tensors(fn, *specs):
         if t is None:
             out.append(None)
             continue
+        if t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
+            out.append(t.data_ptr())
+            continue
         if t.dtype is not dtype or t.numel() < n:
             raise ValueError(f"{fn}: {name} has {t.numel()} elements of {t.dtype}, expected {n} of {dtype}")
         if t.get_device() != dev:
             raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{dev}")
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} is not contiguous")
-        out.append(t.data_ptr())
+        raise ValueError(f"{fn}: {name} is not contiguous")
     return out
 
 
