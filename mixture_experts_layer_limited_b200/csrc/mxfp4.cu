@@ -84,8 +84,8 @@ __device__ __forceinline__ uint32_t mx_block(const uint4& u, uint32_t& scale) {
 constexpr int kMxRows = 8;                                           // rows (warps) per CTA
 constexpr int kMxSteps = 4;                                          // of 256 values per warp
 __global__ void __launch_bounds__(32 * kMxRows)
-mx_quant_rows_kernel(int rows, int K, const uint4* __restrict__ a, int a_rows, const int32_t* __restrict__ src,
-                     uint32_t* __restrict__ q, uint32_t* __restrict__ scale, int32_t* status) {
+mx_quant_rows_kernel(int rows, int K, const uint4* a, int a_rows, const int32_t* src,
+                     uint32_t* q, uint32_t* scale, int32_t* status) {
   launch_dependents_if_small();
   griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -104,7 +104,7 @@ mx_quant_rows_kernel(int rows, int K, const uint4* __restrict__ a, int a_rows, c
 #pragma unroll
   for (int i = 0; i < kMxSteps; ++i) {
     const int c = c0 + 32 * i;
-    u[i] = c < K / 8 && !bad ? __ldg(row + c) : make_uint4(0u, 0u, 0u, 0u);
+    u[i] = c < K / 8 && !bad ? row[c] : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int i = 0; i < kMxSteps; ++i) {
@@ -135,8 +135,8 @@ __device__ __forceinline__ uint32_t mx_bf16x2(uint32_t codes, float sc) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __global__ void __launch_bounds__(32 * kMxRows)
-mx_dequant_rows_kernel(int rows, int K, const uint32_t* __restrict__ q, const uint32_t* __restrict__ scale,
-                       uint4* __restrict__ out) {
+mx_dequant_rows_kernel(int rows, int K, const uint32_t* q, const uint32_t* scale,
+                       uint4* out) {
   launch_dependents_if_small();
   griddep_wait();
   const int lane = threadIdx.x & 31;

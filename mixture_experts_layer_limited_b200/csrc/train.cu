@@ -476,7 +476,7 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 }
 
 // A row's d_row_w: its partial sums, in feature order.
-__device__ __forceinline__ float sum_partials(const float* __restrict__ partial, int n, int rows, int r) {
+__device__ __forceinline__ float sum_partials(const float* partial, int n, int rows, int r) {
   float s = 0.0f;
 #pragma unroll 8
   for (int i = 0; i < n; ++i) s += partial[static_cast<size_t>(i) * rows + r];
@@ -485,8 +485,8 @@ __device__ __forceinline__ float sum_partials(const float* __restrict__ partial,
 // d_row_w where no weight gradients are asked for (else wgrad_kernel does it);
 // rows outside [offsets[0], offsets[groups]) are left as they were.
 __global__ void __launch_bounds__(256)
-row_w_grad_kernel(int rows, int n, const float* __restrict__ partial, const int32_t* __restrict__ offsets, int groups,
-                  float* __restrict__ d_row_w) {
+row_w_grad_kernel(int rows, int n, const float* partial, const int32_t* offsets, int groups,
+                  float* d_row_w) {
   launch_dependents_if_small();
   griddep_wait();
   const int r = blockIdx.x * 256 + threadIdx.x;
@@ -592,7 +592,7 @@ __device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* o
   w.n = i.ni * 256;
   w.N = a.prob[i.p].N;
   w.k0 = off[w.g];
-  w.kn = off[w.g + 1] - w.k0;
+  w.kn = max(off[w.g + 1] - w.k0, 0);                    // a segment that ends before it starts has no rows
   return w;
 }
 
@@ -759,7 +759,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
     uint32_t par = 0;
     for (WgradIter i(a, first, stride); i.t < total; i.next(a, total)) {
       const WgradTile w = wgrad_tile(a, off, i);
-      const int blocks = (max(w.kn, 0) + KB - 1) / KB;
+      const int blocks = (w.kn + KB - 1) / KB;
       if (w.kn & 15) {
         const int st = (stage + blocks - 1) % STAGES;
         const int valid = w.kn - (blocks - 1) * KB;
@@ -797,7 +797,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       const uint32_t acc = lane_addr + (it & 1u) * 256;
       if (!mbar_wait_warp(&tmem_full[it & 1u], (it >> 1) & 1u, abort_flag, a.status, a.wait_ns)) break;
       tc_fence_after();
-      const bool empty = w.kn <= 0;
+      const bool empty = w.kn == 0;
       // adding nothing needs no store, and rows past the matrix have none
       if (!(empty && a.accumulate) && m < pr.M) {
 #pragma unroll 1
@@ -874,10 +874,10 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
 // with ds_e = 0 for experts not chosen. One warp per token: lane j holds slot
 // j, lane l the experts l, l + 32, ... . Bound by its E logits' bytes.
 __global__ void __launch_bounds__(256)
-route_backward_kernel(int T, int E, int k, int scoring, int norm, float scale, const float* __restrict__ logits,
-                      const int32_t* __restrict__ ids, const float* __restrict__ d_w,
-                      const int32_t* __restrict__ slot_to_row, float* __restrict__ d_logits,
-                      __nv_bfloat16* __restrict__ d_logits16, int32_t* status) {
+route_backward_kernel(int T, int E, int k, int scoring, int norm, float scale, const float* logits,
+                      const int32_t* ids, const float* d_w,
+                      const int32_t* slot_to_row, float* d_logits,
+                      __nv_bfloat16* d_logits16, int32_t* status) {
   constexpr int PER = 8;                                           // E <= 256
   launch_dependents_if_small();
   griddep_wait();

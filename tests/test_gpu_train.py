@@ -131,6 +131,25 @@ def test_segments_outside_the_rows_are_cut_and_flagged():
         assert torch.equal(o[k], good[k])
 
 
+def test_segment_that_ends_before_it_starts_is_empty_and_flagged():
+    """Falling offsets: that expert has no rows (no wait runs out), the others
+    keep theirs."""
+    H, I = 256, 128
+    c, off, R, E = _case([20, 30, 6], H, I, seed=18)
+    offs = [0, 20, 5, 5]
+    o = {k: torch.zeros_like(v) for k, v in _backward(c, off, R, E, H, I).items()}
+    ws = torch.empty(N.moe_swiglu_ffn_backward_workspace_size(R, I), dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    N.moe_swiglu_ffn_backward(R, H, c["w13"], c["w2"], E, I, c["a"], c["gu"], c["d_out"],
+                              torch.tensor(offs, dtype=torch.int32, device=DEV), c["row_w"], o["d_a"], o["d_w13"],
+                              o["d_w2"], o["d_row_w"], ws, dev_status=status)
+    assert N.moe_read_device_status(status) == N.MOE_DEVSTAT_BAD_EXPERT_ID
+    good = _backward(c, off, R, E, H, I)
+    assert torch.equal(o["d_a"][:20], good["d_a"][:20]) and torch.equal(o["d_row_w"][:5], good["d_row_w"][:5])
+    for k in ("d_w13", "d_w2"):
+        assert torch.equal(o[k][0], good[k][0]) and not bool(o[k][1:].any())
+
+
 def test_calls_on_two_streams_at_once():
     """Two backward passes in flight at once, a workspace each, give what they
     give one after the other."""
