@@ -440,7 +440,12 @@ MOE_API moe_status moe_gate_up_swiglu_gather(int32_t rows, int32_t H, const moe_
  *     dx = dx_in + d_logits gate   (bf16; dx_in NULL = 0, and may be dx)
  *     d_gate = d_logits^T x        (bf16 or fp32, accumulate, as above)
  *   d_logits_bf16 [T, E]; x [T, H]; gate_w [E, H]; dx or d_gate may be NULL.
+ *   Both run at once: dx is not x's memory.
  *   Limits: H % 256 == 0, E % 16 == 0, 16 <= E <= 256.
+ *
+ * Outputs (and the workspace) of these calls and of the 4-bit ones below that
+ * overlap an input or one another are refused (MOE_ERR_INVALID_ARG), but for
+ * dx_in == dx; moe_route_backward's are not checked.
  * ------------------------------------------------------------------------ */
 MOE_API moe_status moe_gate_up_swiglu_train(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* a,
                               const int32_t* offsets, void* h, void* gu, int32_t* dev_status, void* stream);

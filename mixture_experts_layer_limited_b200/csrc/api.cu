@@ -2,6 +2,7 @@
 // the host, TMA tensor-map encoding, kernel launches. No allocation happens
 // here; every buffer belongs to the caller.
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "mxfp4.cuh"
@@ -276,6 +277,26 @@ moe_status moe_permute(int32_t T, int32_t k, int32_t E, int32_t H, const int32_t
 
 namespace {
 
+// Memory a call reads or writes (ptr may be nullptr), and whether its outputs
+// overlap neither an input nor one another.
+struct Span {
+  const void* ptr;
+  size_t bytes;
+};
+bool overlap(const Span& p, const Span& q) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p.ptr), b = reinterpret_cast<uintptr_t>(q.ptr);
+  return p.ptr && q.ptr && a < b + q.bytes && b < a + p.bytes;
+}
+bool outputs_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return false;
+    for (auto n = o + 1; n != outs.end(); ++n)
+      if (overlap(*o, *n)) return false;
+  }
+  return true;
+}
+
 // Shared checks of the grouped SwiGLU calls; `a` is the GEMM's activation
 // operand (x for the first GEMM, h for the second).
 moe_status check_ffn(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* a,
@@ -534,9 +555,12 @@ moe_status moe_gate_up_swiglu_train(int32_t rows, int32_t H, const moe_ffn_weigh
   if (w->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (!h || !gu || (!offsets && w->groups != 1)) return MOE_ERR_INVALID_ARG;
   if (any_misaligned(offsets, h, gu)) return MOE_ERR_ALIGNMENT;
+  const int I = w->I;
+  const size_t r = static_cast<size_t>(rows);
+  if (!outputs_apart({{h, r * I * 2}, {gu, r * I * 4}}, {{a, r * H * 2}, {w->w13, static_cast<size_t>(w->groups) * I * H * 4}}))
+    return MOE_ERR_INVALID_ARG;
   int nsm = 0;
   if ((s = sm_count(&nsm)) != MOE_OK) return s;
-  const int I = w->I;
   CUtensorMap tmA;
   HalfMaps tmB;
   s = make_train_weight_tmap(&tmA, w->w13, TRAIN_FORWARD, w->tiled, w->groups, H, I, 2);
@@ -642,13 +666,7 @@ moe_status moe_tile_ffn_weights(int32_t H, const moe_ffn_weights* src, void* w13
   if (any_misaligned(src->w13, src->w2, w13_t, w2_t)) return MOE_ERR_ALIGNMENT;
   // the copies are gathers: an output overlapping any input would be read after being written
   const size_t b13 = static_cast<size_t>(src->groups) * 2 * src->I * H * 2, b2 = static_cast<size_t>(src->groups) * H * src->I * 2;
-  auto overlap = [](const void* p, size_t np, const void* q, size_t nq) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return p && q && a < b + nq && b < a + np;
-  };
-  if (overlap(w13_t, b13, src->w13, b13) || overlap(w13_t, b13, src->w2, b2) || overlap(w2_t, b2, src->w13, b13) ||
-      overlap(w2_t, b2, src->w2, b2) || overlap(w13_t, b13, w2_t, b2))
-    return MOE_ERR_INVALID_ARG;
+  if (!outputs_apart({{w13_t, b13}, {w2_t, b2}}, {{src->w13, b13}, {src->w2, b2}})) return MOE_ERR_INVALID_ARG;
   cudaStream_t st = as_stream(stream);
   if (w13_t) {   // 256-row tiles: 128 gate rows, then the same features' 128 up rows
     moe_status s = check_launch(launch_tile_weights(src->w13, w13_t, src->groups, 2 * src->I, H, src->I, st));
@@ -887,6 +905,12 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
   if (workspace_bytes < ws.total) return MOE_ERR_INVALID_ARG;
   if (any_misaligned(a, gu, d_out, offsets, row_w, d_a, d_w13, d_w2, d_row_w, workspace)) return MOE_ERR_ALIGNMENT;
   const int32_t I = w->I;
+  const size_t r = static_cast<size_t>(rows), weight = static_cast<size_t>(w->groups) * I * H;   // values of w2
+  const size_t esize = grad_dtype == MOE_F32 ? 4 : 2;
+  // the products run beside one another: d_a in the place of a or d_out would be read after being written
+  if (!outputs_apart({{d_a, r * H * 2}, {d_w13, weight * 2 * esize}, {d_w2, weight * esize}, {d_row_w, r * 4}, {workspace, ws.total}},
+                     {{a, r * H * 2}, {gu, r * I * 4}, {d_out, r * H * 2}, {row_w, r * 4}, {w->w13, weight * 4}, {w->w2, weight * 2}}))
+    return MOE_ERR_INVALID_ARG;
   // output tiles of the weight gradients are counted in int32
   if (static_cast<long long>(w->groups) * (2 * I / 128) * (H / 256) > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED;
   int nsm = 0;
@@ -985,6 +1009,11 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
   if (!grad_args_ok(grad_dtype, accumulate)) return MOE_ERR_INVALID_ARG;
   if (H % 256 != 0 || E > 256 || E < 16 || E % 16 != 0) return MOE_ERR_UNSUPPORTED;
   if (any_misaligned(d_logits_bf16, x, gate_w, dx_in, dx, d_gate)) return MOE_ERR_ALIGNMENT;
+  const size_t rows_bytes = static_cast<size_t>(T) * H * 2, gate_values = static_cast<size_t>(E) * H;
+  const Span in{dx_in != dx ? dx_in : nullptr, rows_bytes};          // dx_in may be dx, but not overlap it otherwise
+  if (!outputs_apart({{dx, rows_bytes}, {d_gate, gate_values * (grad_dtype == MOE_F32 ? 4 : 2)}},
+                     {{d_logits_bf16, static_cast<size_t>(T) * E * 2}, {x, rows_bytes}, {gate_w, gate_values * 2}, in}))
+    return MOE_ERR_INVALID_ARG;
   int nsm = 0;
   moe_status s = sm_count(&nsm);
   if (s != MOE_OK) return s;
@@ -1029,6 +1058,9 @@ moe_status moe_quantize_mxfp4_rows(int32_t rows, int32_t K, const void* a, int32
   if (rows < 1 || K < 1 || a_rows < 1 || !a || !q || !scale || (!src_rows && a_rows < rows)) return MOE_ERR_INVALID_ARG;
   if (K % 128 != 0) return MOE_ERR_UNSUPPORTED;
   if (any_misaligned(a, src_rows, q, scale)) return MOE_ERR_ALIGNMENT;
+  const size_t n = static_cast<size_t>(rows) * K;
+  if (!outputs_apart({{q, n / 2}, {scale, n / 32}}, {{a, static_cast<size_t>(a_rows) * K * 2}, {src_rows, static_cast<size_t>(rows) * 4}}))
+    return MOE_ERR_INVALID_ARG;
   return check_launch(launch_mx_quant_rows(rows, K, a, a_rows, src_rows, q, scale, dev_status, as_stream(stream)));
 }
 
@@ -1036,6 +1068,8 @@ moe_status moe_dequantize_mxfp4_rows(int32_t rows, int32_t K, const void* q, con
   if (rows < 1 || K < 1 || !q || !scale || !out) return MOE_ERR_INVALID_ARG;
   if (K % 128 != 0) return MOE_ERR_UNSUPPORTED;
   if (any_misaligned(q, scale, out)) return MOE_ERR_ALIGNMENT;
+  const size_t n = static_cast<size_t>(rows) * K;
+  if (!outputs_apart({{out, n * 2}}, {{q, n / 2}, {scale, n / 32}})) return MOE_ERR_INVALID_ARG;
   return check_launch(launch_mx_dequant_rows(rows, K, q, scale, out, as_stream(stream)));
 }
 
@@ -1044,6 +1078,8 @@ moe_status moe_quantize_mxfp4_weights(int32_t batch, int32_t N, int32_t K, const
   if (batch < 1 || N < 1 || K < 1 || !w || !q || !scale) return MOE_ERR_INVALID_ARG;
   if (N % 128 != 0 || K % 128 != 0 || static_cast<long long>(batch) * N > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   if (any_misaligned(w, q, scale)) return MOE_ERR_ALIGNMENT;
+  const size_t n = static_cast<size_t>(batch) * N * K;
+  if (!outputs_apart({{q, n / 2}, {scale, n / 32}}, {{w, n * 2}})) return MOE_ERR_INVALID_ARG;
   return check_launch(launch_mx_quant_weights(batch, N, K, w, q, scale, as_stream(stream)));
 }
 

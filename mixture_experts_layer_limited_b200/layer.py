@@ -379,13 +379,16 @@ class MoELayer:
         """forward() of a bf16 layer that keeps what backward() needs: x itself
         (not to be changed before it), the routing and the pre-activations, in
         the layer's buffers. backward() belongs to the last forward_train(); a
-        forward() in between takes the buffers and ends that. Run the step once
+        forward() in between takes the buffers and ends that (the replay of a
+        captured one as well, which is not noticed here). Run the step once
         before capturing it into a CUDA graph (the buffers are allocated then)."""
         s, T = self.spec, x.shape[0]
         if self.quant or self.gather:
             raise ValueError("forward_train needs a bf16 layer without gather")
         if T > self.T_max or x.dtype != torch.bfloat16 or not x.is_contiguous():
             raise ValueError("x: contiguous bf16 rows, at most T_max of them")
+        if x.untyped_storage().data_ptr() == self.y.untyped_storage().data_ptr():
+            raise ValueError("x is this layer's output buffer, which its forward overwrites")
         t, R = self._train_buffers(), T * s.k
         self.route(x)
         self.permute(x, T)

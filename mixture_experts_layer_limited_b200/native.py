@@ -355,15 +355,16 @@ def moe_swiglu_ffn_backward(rows, H, w13, w2, groups, I, a, gu, d_out, offsets, 
     moe_gate_up_swiglu_train saved; outputs that are None are not computed."""
     bf, f32, gt = torch.bfloat16, torch.float32, _grad("moe_swiglu_ffn_backward", grad_dtype)
     n13, n2 = groups * 2 * I * H, groups * H * I
+    ws_bytes, ws_type = (0, None) if workspace is None else (workspace.numel() * workspace.element_size(), workspace.dtype)
     p13, p2, pa, pgu, pdo, poff, prw, pda, pd13, pd2, pdrw, pws = _tensors(
         "moe_swiglu_ffn_backward", ("w13", w13, n13, bf), ("w2", w2, n2, bf), ("a", a, rows * H, bf),
         ("gu", gu, rows * 2 * I, bf), ("d_out", d_out, rows * H, bf), ("offsets", offsets, groups + 1, torch.int32),
         ("row_w", row_w, rows, f32), ("d_a", d_a, rows * H, bf), ("d_w13", d_w13, n13, gt), ("d_w2", d_w2, n2, gt),
-        ("d_row_w", d_row_w, rows, f32), ("workspace", workspace, 1, workspace.dtype))
+        ("d_row_w", d_row_w, rows, f32), ("workspace", workspace, 1, ws_type))
     w = FFNWeights(p13, p2, None, None, MOE_BF16, groups, I, int(tiled))
     _check("moe_swiglu_ffn_backward", load_library().moe_swiglu_ffn_backward(
         rows, H, ctypes.byref(w), pa, pgu, pdo, poff, prw, pda, pd13, pd2, grad_dtype, int(bool(accumulate)), pdrw,
-        pws, workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
+        pws, ws_bytes, _ptr(dev_status), _stream(stream)))
 
 
 def moe_route_backward(T, E, k, scoring, norm_topk_prob, routed_scaling_factor, logits, topk_ids, d_topk_w,

@@ -136,6 +136,8 @@ def test_training_refusals():
         layer.backward(inp.x[:3], layer.grad_buffers())
     with pytest.raises(ValueError):
         layer.backward(inp.x, {"w13": layer.grad_buffers()["w13"]})
+    with pytest.raises(ValueError):
+        layer.forward_train(layer.forward(inp.x))        # its own output buffer, overwritten before backward()
     inp4, layer4 = _layer(dataclasses.replace(cfg, dtype="mxfp4"))
     with pytest.raises(ValueError):
         layer4.forward_train(inp4.x)

@@ -135,6 +135,41 @@ def test_mxfp4_refusals():
     assert lib.moe_last_cuda_error() == 0
 
 
+@built
+def test_overlapping_outputs_are_refused():
+    """The products of a call run beside one another, so an output in an input's
+    or another output's memory would be read after being written."""
+    lib = N.load_library()
+    at = lambda i: P(0x10000000 * (i + 1))                                # far apart; never dereferenced
+    E, H, I, R = 4, 512, 256, 64
+    w = _w(w13=at(0), w2=at(1))
+
+    def train(a=at(2), h=at(3), gu=at(4)):
+        return lib.moe_gate_up_swiglu_train(R, H, ctypes.byref(w), a, at(5), h, gu, None, None)
+    assert train(h=at(2)) == N.MOE_ERR_INVALID_ARG
+    assert train(gu=P(at(3).value + R * I * 2 - 16)) == N.MOE_ERR_INVALID_ARG
+
+    need = N.moe_swiglu_ffn_backward_workspace_size(R, I)
+
+    def back(d_a=at(6), d13=at(7), d2=at(8), drw=at(9), ws=at(10)):
+        return lib.moe_swiglu_ffn_backward(R, H, ctypes.byref(w), at(2), at(4), at(3), at(5), at(11), d_a, d13, d2,
+                                           N.MOE_BF16, 0, drw, ws, need, None, None)
+    for kw in (dict(d_a=at(2)), dict(d_a=at(3)), dict(d13=at(0)), dict(d2=at(7)), dict(drw=at(11)), dict(ws=at(4)),
+               dict(d_a=P(at(3).value + R * H * 2 - 16)), dict(drw=P(at(10).value + need - 16))):
+        assert back(**kw) == N.MOE_ERR_INVALID_ARG, kw
+
+    def gate(x=at(12), dx_in=at(13), dx=at(14), dg=at(15)):
+        return lib.moe_gate_backward(R, H, 64, at(16), x, at(17), dx_in, dx, dg, N.MOE_BF16, 0, None, None)
+    assert gate(dx=at(12)) == N.MOE_ERR_INVALID_ARG
+    assert gate(dx_in=P(at(14).value + 16)) == N.MOE_ERR_INVALID_ARG      # dx itself, or apart from it
+    assert gate(dg=at(17)) == N.MOE_ERR_INVALID_ARG
+    assert lib.moe_quantize_mxfp4_rows(8, 256, at(0), 8, at(1), at(0), at(2), None, None) == N.MOE_ERR_INVALID_ARG
+    assert lib.moe_quantize_mxfp4_rows(8, 256, at(0), 8, at(1), at(2), at(2), None, None) == N.MOE_ERR_INVALID_ARG
+    assert lib.moe_dequantize_mxfp4_rows(8, 256, at(0), at(1), at(0), None) == N.MOE_ERR_INVALID_ARG
+    assert lib.moe_quantize_mxfp4_weights(1, 128, 256, at(0), at(0), at(1), None) == N.MOE_ERR_INVALID_ARG
+    assert lib.moe_last_cuda_error() == 0
+
+
 # ------------------------------------------------- the tests' own formulas
 def test_backward_formula_against_differences():
     """The float64 formula of the GPU tests: every gradient along random
