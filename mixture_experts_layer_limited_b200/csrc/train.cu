@@ -93,27 +93,28 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc,
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrives on `bar` of both CTAs once every MMA issued so far by this thread is done.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+// Arrives on `bar` of both CTAs once every MMA issued so far by this thread is
+// done. `lead`: the pair's first CTA in the cluster.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, int lead = 0) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3 << lead))
       : "memory");
 }
-// Arrives on the first CTA's copy of `bar`. What the arrival hands over is
+// Arrives on the pair's first CTA's copy of `bar`. What the arrival hands over is
 // shared memory of this SM that the MMAs read in place: a thread that wrote it
 // has made its stores visible to them with fence.proxy.async before, so the
 // arrival itself needs no order beyond this CTA's (a release at cluster scope
 // waits for a memory barrier of the whole GPU: 870 us instead of 790 for the
 // weight gradients of 251 rows on each of 32 experts). The relaxed form is for
 // threads that wrote nothing.
-__device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
+__device__ __forceinline__ void mbar_arrive_first(uint64_t* bar, int lead = 0) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), lead))
                : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_first_relaxed(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), 0))
+__device__ __forceinline__ void mbar_arrive_first_relaxed(uint64_t* bar, int lead = 0) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), lead))
                : "memory");
 }
 // Arrives on `bar` of this CTA once every MMA issued so far by this thread is done.
@@ -131,16 +132,16 @@ __device__ __forceinline__ void umma_commit_first(uint64_t* bar) {
 // barriers.
 template <int STAGES>
 __device__ void pair_drain(uint64_t* full, const uint32_t* loads, const uint32_t* load_bytes, volatile int* abort_flag,
-                           const int* abort_word) {
-  if (!*abort_flag && ld_cluster(abort_word, 1) == 0) return;
+                           const int* abort_word, int lead = 0) {
+  if (!*abort_flag && ld_cluster(abort_word, lead + 1) == 0) return;
   for (int i = 0; i < STAGES; ++i) {
-    const uint32_t mine = loads[i], theirs = ld_cluster(&loads[i], 1);
+    const uint32_t mine = loads[i], theirs = ld_cluster(&loads[i], lead + 1);
     if (mine > theirs)
       asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[i])),
                    "r"(load_bytes[i])
                    : "memory");
     else if (theirs > mine)
-      mbar_arrive_expect_tx(&full[i], ld_cluster(&load_bytes[i], 1));
+      mbar_arrive_expect_tx(&full[i], ld_cluster(&load_bytes[i], lead + 1));
     const uint32_t n = mine > theirs ? mine : theirs;
     if (n) mbar_wait_drain(&full[i], (n - 1) & 1u);
   }
@@ -522,6 +523,8 @@ row_w_grad_kernel(int rows, int n, const float* partial, const int32_t* offsets,
 //
 // Measured on B200 at V3 widths, 32 experts: 256 rows each 777 us (3.6 TB/s
 // written, 930 TFLOP/s), 251 rows 792 us, 16 rows 470 us (6.0 TB/s written).
+// The router's (8192 rows, 256 x 7168: 28 tiles) over 56 pairs: its gradient,
+// with dx, 110 us instead of 120.
 // What was slower at 256 rows: one CTA per tile of 256 x 256 with one
 // accumulator 935 us; the warps storing 16 or 32 bytes a thread themselves 890
 // and 970; 128-row store boxes 808; B's blocks kept for a run of eight tiles,
@@ -583,8 +586,10 @@ struct WgradIter {
 };
 struct WgradTile { int p, g, m, n, N, k0, kn; };
 
-// `off`: the segments' starts in shared memory, cut to the rows there are.
-__device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* off, const WgradIter& i) {
+// `off`: the segments' starts in shared memory, cut to the rows there are; part
+// `part` of SPLIT of the segment's blocks of rows.
+template <int SPLIT>
+__device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* off, const WgradIter& i, int part) {
   WgradTile w;
   w.p = i.p;
   w.g = i.g;
@@ -593,10 +598,17 @@ __device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* o
   w.N = a.prob[i.p].N;
   w.k0 = off[w.g];
   w.kn = max(off[w.g + 1] - w.k0, 0);                    // a segment that ends before it starts has no rows
+  if (SPLIT > 1) {
+    const int blocks = (w.kn + WgradCfg::KB - 1) / WgradCfg::KB;
+    const int from = part * blocks / SPLIT * WgradCfg::KB, to = (part + 1) * blocks / SPLIT * WgradCfg::KB;
+    w.kn = max(min(w.kn, to) - from, 0);
+    w.k0 += from;
+  }
   return w;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WgradCfg::THREADS, 1)
+template <int SPLIT>
+__global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(WgradCfg::THREADS, 1)
 wgrad_kernel(const __grid_constant__ WgradArgs a) {
   using C = WgradCfg;
   constexpr int KB = C::KB, STAGES = C::STAGES, EPIW = C::EPIW;
@@ -611,8 +623,9 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
   volatile int* abort_flag = &sm.abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int first = static_cast<int>(cluster_id_x()), stride = static_cast<int>(gridDim.x) / 2;
+  const int crank = static_cast<int>(cluster_ctarank());
+  const int rank = crank & 1, lead = crank & ~1, part = crank >> 1;   // in the pair; its first CTA; which pair
+  const int first = static_cast<int>(cluster_id_x()), stride = static_cast<int>(gridDim.x) / (2 * SPLIT);
   auto sA = [&](int st) { return sm.stage[st]; };
   auto sB = [&](int st) { return sm.stage[st] + C::PAIR; };
 
@@ -654,6 +667,47 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
   const uint32_t tmem_base = sm.tmem_base;
   const int total = a.prob[0].tiles + (a.n_prob > 1 ? a.prob[1].tiles : 0);
 
+  // 32 features x `cols` columns from c of tile w, one feature a lane, through this warp's box
+  auto store = [&](const WgradTile& w, int c, const float (&v)[32], const float (&v2)[32]) {
+    uint8_t* box = sm.out[warp - 2];                               // 32 rows x 128 B
+    // the last store of this box has been read
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    uint8_t* row = box + lane * 128;
+    if (a.f32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float* f = i < 4 ? v + 8 * i : v2 + 8 * (i - 4);
+        uint4 u;
+        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+        *reinterpret_cast<uint4*>(row + ((i ^ (lane & 7)) << 4)) = u;
+      }
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      const WgradProblem& pr = a.prob[w.p];
+      const int y = w.g * pr.M + w.m + 128 * rank + 32 * (warp & 3);
+      if (a.accumulate)
+        asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];"
+                     ::"l"(reinterpret_cast<uint64_t>(&pr.tmOut)), "r"(smem_u32(box)), "r"(w.n + c), "r"(y)
+                     : "memory");
+      else
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+                     ::"l"(reinterpret_cast<uint64_t>(&pr.tmOut)), "r"(smem_u32(box)), "r"(w.n + c), "r"(y)
+                     : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  };
+  const int cols = a.f32 ? 32 : 64;                                // columns of a box
+
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
@@ -661,7 +715,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       uint32_t phase = 0;
       bool ok = true;
       for (WgradIter i(a, first, stride); i.t < total && ok && !*abort_flag; i.next(a, total)) {
-        const WgradTile w = wgrad_tile(a, off, i);
+        const WgradTile w = wgrad_tile<SPLIT>(a, off, i, part);
         const WgradProblem& pr = a.prob[w.p];
         const int m = w.m + 128 * rank;
         const int nb = w.n / 64 + (w.N - w.n > 128 ? 2 : 1) * rank;    // this CTA's half of B's features
@@ -671,11 +725,11 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
           uint32_t bar;
           if (tail) {
             mbar_arrive_expect_tx(&sm.tail_full[stage], C::STAGE_BYTES);
-            bar = mapa_shared(smem_u32(&sm.tail_full[stage]), rank);
+            bar = mapa_shared(smem_u32(&sm.tail_full[stage]), crank);
             ++sm.tails[stage];
           } else {
             if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::STAGE_BYTES);
-            bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+            bar = mapa_shared(smem_u32(&full_bar[stage]), lead);
             ++sm.loads[stage];
           }
           if (pr.a_flat) {                                         // rows not a whole number of boxes wide
@@ -707,7 +761,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       uint32_t it = 0, full_par = 0, tail_par = 0;                 // parity of each stage's next wait, by barrier
       bool ok = true;
       for (WgradIter i(a, first, stride); i.t < total && ok; i.next(a, total), ++it) {
-        const WgradTile w = wgrad_tile(a, off, i);
+        const WgradTile w = wgrad_tile<SPLIT>(a, off, i, part);
         const uint32_t idesc = make_idesc(1u, 256u, w.N - w.n > 128 ? 256u : 128u) | kIdescAMn | kIdescBMn;
         const uint32_t d0 = tmem_base + (it & 1u) * 256;
         const int even = w.kn / KB, rest = w.kn - even * KB;       // blocks of 64 rows, and the last one's rows
@@ -725,7 +779,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
             umma_bf16_pair(d0, ad + kk * 128, bd + kk * 128, idesc, acc);
             acc = 1;
           }
-          umma_commit_pair(&empty_bar[st]);
+          umma_commit_pair(&empty_bar[st], lead);
           full_par ^= 1u << st;
           if (++st == STAGES) st = 0;
         }
@@ -744,10 +798,10 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
             umma_bf16_pair(d0, ad + kk * 128, bd + kk * 128, idesc, acc);
             acc = 1;
           }
-          umma_commit_pair(&empty_bar[st]);
+          umma_commit_pair(&empty_bar[st], lead);
           if (++st == STAGES) st = 0;
         }
-        if (ok) umma_commit_pair(&tmem_full[it & 1u]);
+        if (ok) umma_commit_pair(&tmem_full[it & 1u], lead);
       }
       // all issued MMAs must finish before TMEM is released
       umma_commit_first(&sm.drain_bar);
@@ -758,7 +812,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
     int stage = 0;
     uint32_t par = 0;
     for (WgradIter i(a, first, stride); i.t < total; i.next(a, total)) {
-      const WgradTile w = wgrad_tile(a, off, i);
+      const WgradTile w = wgrad_tile<SPLIT>(a, off, i, part);
       const int blocks = (w.kn + KB - 1) / KB;
       if (w.kn & 15) {
         const int st = (stage + blocks - 1) % STAGES;
@@ -772,7 +826,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
           for (int b = 0; b < 4; ++b) *reinterpret_cast<uint4*>(base + b * kChunkBytes + i) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive_first(&sm.tail_done[st]);
+        if (lane == 0) mbar_arrive_first(&sm.tail_done[st], lead);
       }
       stage = (stage + blocks) % STAGES;
     }
@@ -786,17 +840,16 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       for (int r = off[0] + blockIdx.x * 32 * EPIW + threadIdx.x - 64; r < hi; r += gridDim.x * 32 * EPIW)
         a.d_row_w[r] = sum_partials(a.partial, a.n_partial, a.rows, r);
     }
-    uint8_t* box = sm.out[warp - 2];                               // 32 rows x 128 B
-    const int cols = a.f32 ? 32 : 64;                              // columns of such a row
     uint32_t it = 0;
     for (WgradIter i(a, first, stride); i.t < total; i.next(a, total), ++it) {
-      const WgradTile w = wgrad_tile(a, off, i);
+      const WgradTile w = wgrad_tile<SPLIT>(a, off, i, part);
       const WgradProblem& pr = a.prob[w.p];
       const int width = w.N - w.n > 128 ? 256 : 128;
       const int m = w.m + 128 * rank + 32 * q;                     // this warp's 32 features of A
       const uint32_t acc = lane_addr + (it & 1u) * 256;
       if (!mbar_wait_warp(&tmem_full[it & 1u], (it >> 1) & 1u, abort_flag, a.status, a.wait_ns)) break;
       tc_fence_after();
+      if (SPLIT > 1) continue;                                     // one tile, summed over its pairs below
       const bool empty = w.kn == 0;
       // adding nothing needs no store, and rows past the matrix have none
       if (!(empty && a.accumulate) && m < pr.M) {
@@ -811,53 +864,70 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = v2[j] = 0.0f;
           }
-          // the last store of this box has been read
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          __syncwarp();
-          uint8_t* row = box + lane * 128;
-          if (a.f32) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) =
-                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float* f = i < 4 ? v + 8 * i : v2 + 8 * (i - 4);
-              uint4 u;
-              __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
-              *reinterpret_cast<uint4*>(row + ((i ^ (lane & 7)) << 4)) = u;
-            }
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            const int y = w.g * pr.M + m;
-            if (a.accumulate)
-              asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];"
-                           ::"l"(reinterpret_cast<uint64_t>(&pr.tmOut)), "r"(smem_u32(box)), "r"(w.n + c), "r"(y)
-                           : "memory");
-            else
-              asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
-                           ::"l"(reinterpret_cast<uint64_t>(&pr.tmOut)), "r"(smem_u32(box)), "r"(w.n + c), "r"(y)
-                           : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
+          store(w, c, v, v2);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[it & 1u]);
+      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[it & 1u], lead);
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (SPLIT == 1 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();                                                  // neither CTA issues anything any more
-  if (rank == 0 && threadIdx.x == 0) pair_drain<STAGES>(sm.full_bar, sm.loads, sm.load_bytes, abort_flag, &sm.abort_flag);
+  cluster_sync();                                                  // no CTA of the cluster issues anything any more
+  if constexpr (SPLIT > 1) {
+    // Pair j gets the others' sums of its 256 / SPLIT columns in the stages, by
+    // now free: [other pair][column][128 features], adds them in that order and stores.
+    constexpr int CW = 256 / SPLIT;
+    const bool epi = warp >= 2 && warp < 2 + EPIW;
+    const int q = warp & 3, half = (warp - 2) / 4;
+    const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    float* got = reinterpret_cast<float*>(sm.stage[0]);
+    const WgradIter i(a, first, stride);
+    const WgradTile w = wgrad_tile<SPLIT>(a, off, i, part);
+    tc_fence_after();
+    if (epi) {
+      for (int d = 1; d < SPLIT; ++d) {
+        const int to = (part + d) % SPLIT, slot = part < to ? part : part - 1;
+        const uint32_t dst = mapa_shared(smem_u32(got + (slot * CW) * 128 + 32 * q + lane), 2 * to + rank);
+        for (int c = 32 * half; c < CW; c += 64) {
+          float v[32];
+          tmem_ld32(acc + to * CW + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + (c + j) * 512), "f"(w.kn ? v[j] : 0.0f) : "memory");
+        }
+      }
+    }
+    cluster_sync();
+    const int m = w.m + 128 * rank + 32 * q;
+    if (epi && !*abort_flag && m < a.prob[w.p].M) {
+      for (int c = half * cols; c < CW; c += 2 * cols) {
+        float v[32], v2[32];
+        tmem_ld32(acc + part * CW + c, v);
+        if (!a.f32) tmem_ld32(acc + part * CW + c + 32, v2);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (!w.kn) v[j] = 0.0f;
+          if (!w.kn || a.f32) v2[j] = 0.0f;
+          for (int o = 0; o < SPLIT - 1; ++o) {
+            const float* f = got + (o * CW + c + j) * 128 + 32 * q + lane;
+            v[j] += f[0];
+            if (!a.f32) v2[j] += f[32 * 128];
+          }
+        }
+        store(w, part * CW + c, v, v2);
+      }
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (rank == 0 && threadIdx.x == 0) pair_drain<STAGES>(sm.full_bar, sm.loads, sm.load_bytes, abort_flag, &sm.abort_flag, lead);
   cluster_sync();                                                  // nothing of either CTA is used any more
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
@@ -993,17 +1063,32 @@ cudaError_t launch_route_backward(int T, int E, int k, int scoring, int norm, fl
                       slot_to_row, d_logits, static_cast<__nv_bfloat16*>(d_logits16), status);
 }
 
-cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
+template <int SPLIT>
+static cudaError_t wgrad(const WgradArgs& a, int clusters, cudaStream_t stream) {
   constexpr size_t smem = sizeof(WgradSmem);
   static_assert(smem <= 232448, "wgrad_kernel's shared memory exceeds an SM's");
-  cudaError_t e = cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int tiles = a.prob[0].tiles + (a.n_prob > 1 ? a.prob[1].tiles : 0);
+  return launch_after(wgrad_kernel<SPLIT>, 2 * SPLIT * clusters, WgradCfg::THREADS, smem, stream, a);
+}
+cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
+  int tiles = 0;
+  bool wide = true;                                    // whole tiles of 256 columns
+  for (int p = 0; p < a.n_prob; ++p) {
+    tiles += a.prob[p].tiles;
+    wide = wide && a.prob[p].N % 256 == 0;
+  }
   // where the kernel before leaves most SMs idle, this one takes those alone: a
   // pair that had to wait for that one's end would do its share of the tiles late
   const int all = num_sms / 2, room = a.after && 2 * a.beside <= all ? all - a.beside : all;
-  const int pairs = room < tiles ? room : tiles;
-  return launch_after(wgrad_kernel, 2 * pairs, WgradCfg::THREADS, smem, stream, a);
+  // Few tiles of many rows (the router's): each split over two or four pairs, as
+  // long as all have room at once (larger clusters leave some SMs of a die out)
+  // and 256 rows a pair and segment.
+  const int most = room < all * 7 / 8 ? room : all * 7 / 8, rows = a.rows / a.groups;
+  if (wide && 4 * tiles <= most && rows >= 4 * 256) return wgrad<4>(a, tiles, stream);
+  if (wide && 2 * tiles <= most && rows >= 2 * 256) return wgrad<2>(a, tiles, stream);
+  return wgrad<1>(a, room < tiles ? room : tiles, stream);
 }
 
 }  // namespace moe

@@ -389,6 +389,57 @@ def test_gate_backward(T, H, E):
     assert bool(((acc.to(F64) - 1 - ref).abs() <= 2 * F32_U * (1 + ref.abs()) + T * F32_U * (L.abs().T @ X.abs())).all())
 
 
+# ---------------------------- few weight-gradient tiles of many rows: split over rows
+@pytest.mark.parametrize("T,H,E", [(1500, 512, 48), (1023, 256, 256), (2077, 1024, 16), (4100, 256, 176), (3001, 7168, 64)])
+def test_gate_backward_of_many_rows(T, H, E):
+    g = _gen(T)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF)
+    dl, x = n(T, E), n(T, H)
+    ref, mag = dl.to(F64).T @ x.to(F64), dl.to(F64).abs().T @ x.to(F64).abs()
+    dg = torch.empty(E, H, dtype=BF, device=DEV)
+    N.moe_gate_backward(T, H, E, dl, x, None, None, None, dg)
+    assert bool(((dg.to(F64) - ref).abs() <= BF16_U * ref.abs() * 1.01 + T * F32_U * mag).all())
+    acc = torch.ones(E, H, device=DEV)
+    for k in (1, 2):                                                      # adds again
+        N.moe_gate_backward(T, H, E, dl, x, None, None, None, acc, grad_dtype=N.MOE_F32, accumulate=True)
+        assert bool(((acc.to(F64) - 1 - k * ref).abs() <= 2 * k * F32_U * (1 + k * ref.abs()) + k * T * F32_U * mag).all())
+    again = torch.empty_like(dg)
+    N.moe_gate_backward(T, H, E, dl, x, None, None, None, again)
+    assert torch.equal(dg, again)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("counts,H,I", [([1500, 601], 256, 256), ([1100], 512, 256), ([5, 2500, 0], 256, 512),
+                                        ([1, 40, 1200], 256, 256)])
+def test_backward_of_few_long_segments(counts, H, I, f32):
+    c, off, R, E = _case(counts, H, I, seed=41)
+    _check(_backward(c, off, R, E, H, I, f32=f32), c, off, H, I, f32)
+
+
+def test_split_weight_gradient_gives_up_and_recovers():
+    """The wait limit in a weight gradient whose tiles several pairs share."""
+    T, H, E = 2000, 512, 64
+    g = _gen(43)
+    dl, x = (torch.randn(T, n, generator=g, device=DEV).to(BF) for n in (E, H))
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def run():
+        dg = torch.zeros(E, H, dtype=BF, device=DEV)
+        N.moe_gate_backward(T, H, E, dl, x, None, None, None, dg, dev_status=status)
+        return dg, N.moe_read_device_status(status)
+    before, st = run()
+    assert st == 0
+    N.moe_set_wait_limit_ns(5)
+    try:
+        _, st = run()
+    finally:
+        N.moe_set_wait_limit_ns(0)
+    assert st == N.MOE_DEVSTAT_TIMEOUT
+    status.zero_()
+    after, st = run()
+    assert st == 0 and torch.equal(before, after)
+
+
 # -------------------------------------------------- bounded waits time out
 @pytest.mark.parametrize("call", ["forward", "backward", "gate"])
 def test_wait_limit_runs_out_then_the_same_call_is_correct(call):
