@@ -437,30 +437,44 @@ void mx_tile(int32_t rows, int32_t groups, MxGemmArgs* g) {
   g->stages = g->bn_max <= 64 ? 4 : 3;
 }
 
+// A 4-bit weight's codes, w13 as [2 groups][I] rows (a gate block and the same
+// features' up block lie I rows apart), w2 as [groups * H / 128][128], in boxes of
+// 2 x 128 rows of 128 bytes; its scales, 512 bytes per 128 x 128 values, in boxes
+// of the same 256 rows x 256 values.
+moe_status make_mx_weight_tmaps(MxMaps* m, bool gate_up, const moe_ffn_weights* w, int32_t H) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
+  const uint64_t K = gate_up ? H : w->I, n = gate_up ? w->I : 128;
+  const uint64_t blocks = gate_up ? 2 * static_cast<uint64_t>(w->groups) : static_cast<uint64_t>(w->groups) * (H / 128);
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  cuuint64_t dims[3] = {K / 2, n, blocks}, strides[2] = {K / 2, K / 2 * n};
+  cuuint32_t box[3] = {128, 128, 2};
+  CUresult r = enc(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(gate_up ? w->w13 : w->w2), dims, strides, box,
+                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
+  const uint64_t kb = K / 128, sn = gate_up ? w->I / 128 : blocks, sb = gate_up ? blocks : 1;
+  cuuint64_t sdims[4] = {128, kb, sn, sb}, sstrides[3] = {512, 512 * kb, 512 * kb * sn};
+  cuuint32_t sbox[4] = {128, 2, gate_up ? 1u : 2u, gate_up ? 2u : 1u};
+  r = enc(&m->w_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<float*>(gate_up ? w->w13_scale : w->w2_scale), sdims,
+          sstrides, sbox, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
+  return MOE_OK;
+}
+
 // One 4-bit grouped GEMM (scales as moe_quantize_mxfp4_rows / _weights lay them out).
 moe_status run_mx(bool gate_up, int32_t rows, int32_t H, const moe_ffn_weights* w, const void* act, const void* act_scale,
                   const int32_t* offsets, const float* row_w, void* out, void* out_scale, int32_t* dev_status,
                   cudaStream_t st, int nsm) {
   const int32_t I = w->I, K = gate_up ? H : I;
-  const uint64_t a_rows = static_cast<uint64_t>(w->groups) * (gate_up ? 2 * I : H);
-  CUtensorMap tmA;
-  TokenMaps tmB;
-  moe_status s = make_tmap(&tmA, gate_up ? w->w13 : w->w2, true, K / 2, a_rows, gate_up ? 128 : 256);
-  if (s != MOE_OK) return s;
-  for (int i = 0; i < kTokBoxes; ++i)
-    if ((s = make_tmap(&tmB.box[i], act, true, K / 2, rows, 256u >> i)) != MOE_OK) return s;
   MxGemmArgs g;
   g.rows = rows;
   g.K = K;
   g.groups = w->groups;
   g.offsets = offsets;
-  g.a_rows_per_group = gate_up ? 2 * I : H;
   g.n_mblk = gate_up ? I / 128 : H / 256;
-  g.mblk_stride = gate_up ? 128 : 256;
-  g.sub1_off = gate_up ? I : 128;
-  g.a_one_box = gate_up ? 0 : 1;
   mx_tile(rows, w->groups, &g);
-  g.a_scale = reinterpret_cast<const uint8_t*>(gate_up ? w->w13_scale : w->w2_scale);
   g.b_scale = static_cast<const uint32_t*>(act_scale);
   g.row_w = row_w;
   g.out = out;
@@ -468,7 +482,12 @@ moe_status run_mx(bool gate_up, int32_t rows, int32_t H, const moe_ffn_weights* 
   g.out_scale = static_cast<uint8_t*>(out_scale);
   g.status = dev_status;
   g.wait_ns = wait_limit();
-  return check_launch(launch_mx_gemm(gate_up, tmA, tmB, g, nsm, st));
+  MxMaps m;
+  moe_status s = make_mx_weight_tmaps(&m, gate_up, w, H);
+  if (s != MOE_OK) return s;
+  for (int i = 0; i < g.bn_max / 16; ++i)
+    if ((s = make_tmap(&m.rows[i], act, true, K / 2, rows, 16 * (i + 1))) != MOE_OK) return s;
+  return check_launch(launch_mx_gemm(gate_up, m, g, nsm, st));
 }
 
 moe_status run_gate_up(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* a,

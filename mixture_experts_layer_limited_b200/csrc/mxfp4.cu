@@ -222,11 +222,21 @@ __device__ __forceinline__ uint32_t mxf4_idesc(uint32_t M, uint32_t N, uint32_t 
   return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 7) << 27) | ((2 * pair) << 4) | ((2 * pair) << 29);
 }
 
-__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(smem_dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t t, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(t), "l"(policy)
+      : "memory");
 }
 
 constexpr int kMxEpi = 8;                                            // epilogue warps
@@ -239,8 +249,8 @@ __host__ __device__ constexpr uint32_t mx_stage_bytes(int bn) { return kMxA + kM
 // Tiles as in the forward GEMMs: 256 weight rows (gate and up rows of 128
 // features, or 256 rows of w2) as the MMA's A, up to bn_max rows of a segment
 // as B, accumulated side by side in TMEM columns [0, bn) and [bn, 2 bn). A
-// stage is 256 values of K: the codes by TMA into shared memory, the weights'
-// scales by bulk copies beside them, the rows' from L2. Four warps, one for each
+// stage is 256 values of K: the weights' codes, their scales and the rows' codes
+// by TMA, one box each, into shared memory, the rows' scales from L2. Four warps, one for each
 // quarter of the TMEM lanes, then write all scales to 32 TMEM columns of the
 // stage's own (2 bn + 32 * stage ..): lane l of column c has the word (four
 // scales, 128 values) of row 32 c + l, the same in all four quarters. (Copied
@@ -252,7 +262,7 @@ __host__ __device__ constexpr uint32_t mx_stage_bytes(int bn) { return kMxA + kM
 // At a few rows per expert the weights' bytes bound it (4.25 bits a value).
 template <bool GATE_UP>
 __global__ void __launch_bounds__(kMxThreads, 1)
-mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ TokenMaps tmB, const MxGemmArgs a) {
+mx_gemm_kernel(const __grid_constant__ MxMaps maps, const MxGemmArgs a) {
   extern __shared__ __align__(1024) uint8_t dsmem[];
   __shared__ SegSched sched;
   __shared__ __align__(16) float tile_s[kMxEpi][32 * 33];
@@ -287,8 +297,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    for (int i = 0; i < kTokBoxes; ++i) tma_prefetch_desc(&tmB.box[i]);
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.w_scale);
+    for (int i = 0; i < a.bn_max / 16; ++i) tma_prefetch_desc(&maps.rows[i]);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_base_s, 512);
@@ -315,26 +326,19 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       int g = 0;
       for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x) {
         const SegTile ti = decode_tile(sched, sp, t, g);
-        const int row0 = ti.g * a.a_rows_per_group + ti.mb * a.mblk_stride;
-        const int row1 = row0 + a.sub1_off;
-        const uint8_t* sf0 = a.a_scale + static_cast<size_t>(row0 / 128) * k128 * 512;
-        const uint8_t* sf1 = a.a_scale + static_cast<size_t>(row1 / 128) * k128 * 512;
+        // the tile's weight rows: GATE_UP [2 groups][I], else [groups * H / 128][128]
+        const int y = GATE_UP ? ti.mb * 128 : 0, z = GATE_UP ? 2 * ti.g : 2 * (ti.g * a.n_mblk + ti.mb);
+        const CUtensorMap* mB = &maps.rows[ti.N / 16 - 1];
         const uint64_t pol_w = ti.ntb > 1 ? pol_reuse : pol_once;
         bool ok = true;
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag, a.status, a.wait_ns)) { ok = false; break; }
           uint64_t* fb = &full_bar[stage];
-          const uint32_t sf_bytes = k128 - 2 * kb >= 2 ? 1024u : 512u;
-          mbar_arrive_expect_tx(&sfa_bar[stage], 2 * sf_bytes);
-          bulk_load(sSfa(stage), sf0 + kb * 1024, sf_bytes, &sfa_bar[stage]);
-          bulk_load(sSfa(stage) + 1024, sf1 + kb * 1024, sf_bytes, &sfa_bar[stage]);
+          mbar_arrive_expect_tx(&sfa_bar[stage], kMxSfa);
+          tma_load_4d(sSfa(stage), &maps.w_scale, &sfa_bar[stage], 0, 2 * kb, GATE_UP ? ti.mb : z, GATE_UP ? z : 0, pol_w);
           mbar_arrive_expect_tx(fb, kMxA + static_cast<uint32_t>(ti.N) * 128u);
-          tma_load_2d(sA(stage), &tmA, fb, kb * 128, row0, pol_w);
-          if (!a.a_one_box) tma_load_2d(sA(stage) + 128 * 128, &tmA, fb, kb * 128, row1, pol_w);
-          uint8_t* bdst = sB(stage);
-          load_token_rows(ti.N, [&](int which, int off) {
-            tma_load_2d(bdst + off * 128, &tmB.box[which], fb, kb * 128, ti.row0 + off, pol_x);
-          });
+          tma_load_3d(sA(stage), &maps.w, fb, kb * 128, y, z, pol_w);
+          tma_load_2d(sB(stage), mB, fb, kb * 128, ti.row0, pol_x);
           issued_parity[stage] = static_cast<int>(phase);
           if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
@@ -520,13 +524,12 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- launches
-cudaError_t launch_mx_gemm(bool gate_up, const CUtensorMap& tmA, const TokenMaps& tmB, const MxGemmArgs& a, int grid,
-                           cudaStream_t stream) {
+cudaError_t launch_mx_gemm(bool gate_up, const MxMaps& maps, const MxGemmArgs& a, int grid, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(a.stages) * mx_stage_bytes(a.bn_max) + 1024;
   auto kern = gate_up ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_after(kern, grid, kMxThreads, smem, stream, tmA, tmB, a);
+  return launch_after(kern, grid, kMxThreads, smem, stream, maps, a);
 }
 
 static dim3 mx_rows_grid(int rows, int K) {

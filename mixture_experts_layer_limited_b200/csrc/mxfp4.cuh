@@ -9,14 +9,9 @@ namespace moe {
 struct MxGemmArgs {
   int32_t rows = 0, K = 0, groups = 1;
   const int32_t* offsets = nullptr;    // [groups + 1] or nullptr (one segment)
-  int32_t a_rows_per_group = 0;        // weight rows per group (2I or H)
   int32_t n_mblk = 0;                  // tiles of 256 weight rows per group
-  int32_t mblk_stride = 0;             // weight-row stride between tiles (128 / 256)
-  int32_t sub1_off = 0;                // weight-row offset of a tile's second 128 rows (I / 128)
-  int32_t a_one_box = 0;               // a tile's 256 weight rows are contiguous
-  int32_t bn_max = 32;                 // rows per tile at most: 32, 64, 128 or 192
+  int32_t bn_max = 32;                 // rows per tile at most: 32, 64 or 192
   int32_t stages = 4;
-  const uint8_t* a_scale = nullptr;    // [groups, a_rows_per_group / 128, K / 128, 512]
   const uint32_t* b_scale = nullptr;   // [K / 128, rows], four scale bytes each
   const float* row_w = nullptr;        // down: [rows] or nullptr
   void* out = nullptr;                 // gate/up: codes [rows, out_ld / 2]; down: bf16 [rows, out_ld]
@@ -25,8 +20,14 @@ struct MxGemmArgs {
   int32_t* status = nullptr;
   uint64_t wait_ns = kDefaultWaitLimitNs;
 };
-cudaError_t launch_mx_gemm(bool gate_up, const CUtensorMap& tmA, const TokenMaps& tmB, const MxGemmArgs& a, int grid,
-                           cudaStream_t stream);
+// What a stage loads, a box each: a block of 256 values (128 bytes) of K
+constexpr int kMxRowBoxes = 12;
+struct MxMaps {
+  CUtensorMap w;                       // of 2 x 128 weight rows: gate and up of 128 features, or 256 rows of w2
+  CUtensorMap w_scale;                 // their scales
+  CUtensorMap rows[kMxRowBoxes];       // of 16 (i + 1) rows, up to bn_max
+};
+cudaError_t launch_mx_gemm(bool gate_up, const MxMaps& maps, const MxGemmArgs& a, int grid, cudaStream_t stream);
 // src: row r of the result is row src[r] of a [a_rows, K] (nullptr: row r)
 cudaError_t launch_mx_quant_rows(int rows, int K, const void* a, int a_rows, const int32_t* src, void* q, void* scale,
                                  int32_t* status, cudaStream_t stream);

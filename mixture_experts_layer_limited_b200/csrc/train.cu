@@ -1083,11 +1083,12 @@ cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   // pair that had to wait for that one's end would do its share of the tiles late
   const int all = num_sms / 2, room = a.after && 2 * a.beside <= all ? all - a.beside : all;
   // Few tiles of many rows (the router's): each split over two or four pairs, as
-  // long as all have room at once (larger clusters leave some SMs of a die out)
-  // and 256 rows a pair and segment.
-  const int most = room < all * 7 / 8 ? room : all * 7 / 8, rows = a.rows / a.groups;
-  if (wide && 4 * tiles <= most && rows >= 4 * 256) return wgrad<4>(a, tiles, stream);
-  if (wide && 2 * tiles <= most && rows >= 2 * 256) return wgrad<2>(a, tiles, stream);
+  // long as all have room at once (148 SMs take 33 clusters of four CTAs or 15 of
+  // eight: 16 tiles of 2048 rows in two turns of the latter 25 us) and 256 rows a
+  // pair and segment.
+  const int rows = a.rows / a.groups;
+  if (wide && 4 * tiles <= room && tiles <= num_sms * 15 / 148 && rows >= 4 * 256) return wgrad<4>(a, tiles, stream);
+  if (wide && 2 * tiles <= room && tiles <= num_sms * 33 / 148 && rows >= 2 * 256) return wgrad<2>(a, tiles, stream);
   return wgrad<1>(a, room < tiles ? room : tiles, stream);
 }
 
