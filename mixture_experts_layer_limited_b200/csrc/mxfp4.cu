@@ -291,7 +291,7 @@ mx_gemm_kernel(const __grid_constant__ MxMaps maps, const MxGemmArgs a) {
       issued_parity[i] = -1;
     }
     mbar_init(&tmem_full, 1);
-    mbar_init(&tmem_empty, 32 * kMxEpi);
+    mbar_init(&tmem_empty, kMxEpi);                                  // one arrival per epilogue warp
     mbar_init(&drain_bar, 1);
     abort_flag = 0;
     fence_barrier_init();
@@ -435,8 +435,7 @@ mx_gemm_kernel(const __grid_constant__ MxMaps maps, const MxGemmArgs a) {
     }
   } else if (warp >= 8) {
     const int q = warp & 3;
-    const int c0 = (warp - 8) / 4;
-    constexpr int cstep = kMxEpi / 4;
+    const int half = (warp - 8) / 4;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     float* ts = tile_s[warp - 8];
     uint32_t it = 0;
@@ -444,15 +443,28 @@ mx_gemm_kernel(const __grid_constant__ MxMaps maps, const MxGemmArgs a) {
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
       const SegTile ti = decode_tile(sched, sp, t, g);
       const int nchunk = (ti.N + 31) / 32;
+      float* ws = ts + 512;                                          // down: the rows' weights, behind the store tile
+      if (!GATE_UP) {
+        for (int r = lane; r < 32 * nchunk; r += 32)
+          ws[r] = r < ti.n_valid ? (a.row_w ? __ldg(a.row_w + ti.row0 + r) : 1.0f) : 0.0f;
+        __syncwarp();
+      }
       if (!mbar_wait_warp(&tmem_full, it & 1u, &abort_flag, a.status, a.wait_ns)) break;
       tc_fence_after();
+      auto done_reading = [&] {                                      // the next tile's MMAs may start
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tmem_empty);
+      };
       if (GATE_UP) {
+        if (half >= nchunk) done_reading();
         uint8_t* out = reinterpret_cast<uint8_t*>(a.out);
-        for (int c = c0; c < nchunk; c += cstep) {
+        for (int c = half; c < nchunk; c += 2) {
           float g[32], u[32];
           tmem_ld32(lane_addr + c * 32, g);
           tmem_ld32(lane_addr + bn + c * 32, u);
           tmem_ld_wait();
+          if (c + 2 >= nchunk) done_reading();
 #pragma unroll
           for (int j = 0; j < 32; ++j) ts[j * 33 + lane] = silu(g[j]) * u[j];
           __syncwarp();
@@ -485,27 +497,38 @@ mx_gemm_kernel(const __grid_constant__ MxMaps maps, const MxGemmArgs a) {
       } else {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
         __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(ts);
-        for (int c = c0; c < nchunk; c += cstep) {
-          const int row0 = ti.row0 + c * 32, n_rows = ti.n_valid - c * 32;
-          float w[8];
-          frag_row_values(a.row_w ? a.row_w + row0 : nullptr, n_rows, lane, 1.0f, w);
+        // this warp: 32 features of sub-tile `half`, all chunks of rows; read (four
+        // chunks held at once), then stored while the next tile's products run
+        const uint32_t acc = lane_addr + half * bn;
+        const int feat0 = ti.mb * 256 + half * 128 + 32 * q;
+        uint32_t p[4][16];
+        auto read = [&](int c, uint32_t (&to)[16]) {
+          float v[32];
+          tmem_ld_frag(acc + c * 32, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            float v[32];
-            tmem_ld_frag(lane_addr + s * bn + c * 32, v);
-            tmem_ld_wait();
-            uint32_t p[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int i = (k >> 1) & 3;
-              p[k] = pack_bf16(v[2 * k] * w[2 * i], v[2 * k + 1] * w[2 * i + 1]);
-            }
-            store_frag(stg, p, lane, out, static_cast<size_t>(a.out_ld), row0, n_rows, ti.mb * 256 + s * 128 + 32 * q);
+          for (int k = 0; k < 16; ++k) {
+            const float2 w = *reinterpret_cast<const float2*>(ws + c * 32 + frag_row(lane, (k >> 1) & 3, 0));
+            to[k] = pack_bf16(v[2 * k] * w.x, v[2 * k + 1] * w.y);
           }
-        }
+        };
+        auto put = [&](int c, const uint32_t (&from)[16]) {
+          store_frag(stg, from, lane, out, static_cast<size_t>(a.out_ld), ti.row0 + c * 32, ti.n_valid - c * 32, feat0);
+        };
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < nchunk) read(c, p[c]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (c + 4 < nchunk) {
+            put(c, p[c]);
+            read(c + 4, p[c]);
+          }
+        done_reading();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < nchunk) put(c + 4 < nchunk ? c + 4 : c, p[c]);
       }
-      tc_fence_before();
-      mbar_arrive(&tmem_empty);
     }
   }
 
