@@ -7,6 +7,7 @@ fallback.
 """
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -102,9 +103,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_bias_update": [_I, _I, _I, _P, _P, ctypes.c_float, _P, _P],
         "moe_aux_loss_workspace_size": [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)],
         "moe_aux_loss": [_I, _I, _I, _I, _I, _P, _P, ctypes.c_float, _P, _P, ctypes.c_size_t, _P, _P],
-        "moe_gate_up_swiglu_train": [_I, _I, ctypes.POINTER(FFNWeights), _P, _P, _P, _P, _P, _P],
+        "moe_gate_up_swiglu_train": [_I, _I, _P, _P, _P, _P, _P, _P, _P],
         "moe_swiglu_ffn_backward_workspace_size": [_I, _I, ctypes.POINTER(ctypes.c_size_t)],
-        "moe_swiglu_ffn_backward": [_I, _I, ctypes.POINTER(FFNWeights), _P, _P, _P, _P, _P, _P, _P, _P, _I, _I,
+        "moe_swiglu_ffn_backward": [_I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I,
                                     _P, _P, ctypes.c_size_t, _P, _P],
         "moe_route_backward": [_I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P],
         "moe_gate_backward": [_I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P],
@@ -142,11 +143,13 @@ def _ptr(t: Optional[torch.Tensor]):
 # The current stream's handle of a device; torch.cuda.current_stream() builds a
 # Stream object for it, 3 of the 10 us a small call takes on the host.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# likewise the current device's index, once a tensor on one exists
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream=None):
     if stream is None and _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
@@ -159,10 +162,18 @@ def _check(fn: str, status: int):
         raise MoEError(fn, status, detail)
 
 
+_pack_weights = struct.Struct("PPPPiiii").pack
+
+
+def _weights(w13, w2, groups, I, tiled):
+    """A bf16 FFNWeights' bytes (a ctypes.Structure takes a microsecond to build)."""
+    return _pack_weights(w13 or 0, w2 or 0, 0, 0, MOE_BF16, groups, I, int(tiled))
+
+
 def _tensors(fn, *specs):
     """(name, tensor or None, elements, dtype) -> device pointers, after a check
     of every tensor's device, type, layout and size."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     out = []
     for name, t, n, dtype in specs:
         if t is None:
@@ -336,9 +347,8 @@ def moe_gate_up_swiglu_train(rows, H, w13, groups, I, a, offsets, h, gu, dev_sta
     p13, pa, poff, ph, pgu = _tensors(
         "moe_gate_up_swiglu_train", ("w13", w13, groups * 2 * I * H, bf), ("a", a, rows * H, bf),
         ("offsets", offsets, groups + 1, torch.int32), ("h", h, rows * I, bf), ("gu", gu, rows * 2 * I, bf))
-    w = FFNWeights(p13, None, None, None, MOE_BF16, groups, I, int(tiled))
     _check("moe_gate_up_swiglu_train", load_library().moe_gate_up_swiglu_train(
-        rows, H, ctypes.byref(w), pa, poff, ph, pgu, _ptr(dev_status), _stream(stream)))
+        rows, H, _weights(p13, None, groups, I, tiled), pa, poff, ph, pgu, _ptr(dev_status), _stream(stream)))
 
 
 def moe_swiglu_ffn_backward_workspace_size(rows, I) -> int:
@@ -361,9 +371,8 @@ def moe_swiglu_ffn_backward(rows, H, w13, w2, groups, I, a, gu, d_out, offsets, 
         ("gu", gu, rows * 2 * I, bf), ("d_out", d_out, rows * H, bf), ("offsets", offsets, groups + 1, torch.int32),
         ("row_w", row_w, rows, f32), ("d_a", d_a, rows * H, bf), ("d_w13", d_w13, n13, gt), ("d_w2", d_w2, n2, gt),
         ("d_row_w", d_row_w, rows, f32), ("workspace", workspace, 1, ws_type))
-    w = FFNWeights(p13, p2, None, None, MOE_BF16, groups, I, int(tiled))
     _check("moe_swiglu_ffn_backward", load_library().moe_swiglu_ffn_backward(
-        rows, H, ctypes.byref(w), pa, pgu, pdo, poff, prw, pda, pd13, pd2, grad_dtype, int(bool(accumulate)), pdrw,
+        rows, H, _weights(p13, p2, groups, I, tiled), pa, pgu, pdo, poff, prw, pda, pd13, pd2, grad_dtype, int(bool(accumulate)), pdrw,
         pws, ws_bytes, _ptr(dev_status), _stream(stream)))
 
 
