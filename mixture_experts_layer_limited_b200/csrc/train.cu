@@ -163,7 +163,9 @@ __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f
 //     and the four stages loaded meanwhile hide the epilogue.
 //   SUBS = 1 (dh0, and d_a-like products of K <= 512): two accumulators, so that
 //     the epilogue, which is long beside so few products, overlaps the next
-//     tile's MMAs.
+//     tile's MMAs. A long dh0 comes in parts (hidden_parts): the first in one
+//     accumulator, each further one in the other, from where the epilogue warps add
+//     it to the first (in TMEM); then the next tile begins in the free one.
 // Measured on B200, this kernel's dh0 and d_a products at V3 widths, 256 rows
 // on each of 32 experts, and at V2-Lite's layer: one CTA per tile of 256 x 256
 // with one accumulator 365 / 445 and 374 / 253 us; SUBS = 1 303 / 568 and
@@ -246,6 +248,7 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   const uint32_t tmem_base = sm.tmem_base;
   const int total = sm.sched.tile_start[a.groups];
   const int nk = (a.K + KB - 1) / KB;
+  const int parts = MODE == TRAIN_HIDDEN ? a.parts : 1;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -309,16 +312,34 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       uint32_t it = 0, phase = 0;
       bool ok = true;
       int group = 0;
+      uint32_t joins = 0;                                          // parts joined so far
       for (int t = first; t < total && ok; t += stride, ++it) {
         const SegTile ti = decode_tile(sm.sched, sp, t, group);
         const uint32_t idesc = make_idesc(1u, 256u, static_cast<uint32_t>(ti.N)) | (MODE == TRAIN_FORWARD ? 0u : kIdescAMn);
         const uint32_t ac = it % ACCS, ac_ph = (it / ACCS) & 1u;
-        const uint32_t d0 = tmem_base + ac * 256;
-        ok = mbar_wait(&tmem_empty[ac], ac_ph ^ 1u, abort_flag, a.status, a.wait_ns);
+        uint32_t d0 = tmem_base + ac * 256;
+        if (parts == 1)
+          ok = mbar_wait(&tmem_empty[ac], ac_ph ^ 1u, abort_flag, a.status, a.wait_ns);
+        else if (it > 0)                                           // the tile before has joined its last part
+          ok = mbar_wait(&tmem_empty[0], (joins - 1) & 1u, abort_flag, a.status, a.wait_ns);
         if (!ok) break;
         tc_fence_after();
         uint32_t acc = 0;
+        int part = 0, part_end = nk / parts;
         for (int kb = 0; kb < nk; ++kb) {
+          if (MODE == TRAIN_HIDDEN && parts > 1 && kb == part_end) {
+            // the next part, in the other accumulator, once that is free
+            if (part++ > 0) umma_commit_pair(&tmem_full[0]);
+            part_end = (part + 1) * nk / parts;
+            if (part > 1)
+              ok = mbar_wait(&tmem_empty[0], joins++ & 1u, abort_flag, a.status, a.wait_ns);
+            else if (it > 0)
+              ok = mbar_wait(&tmem_empty[1], (it - 1) & 1u, abort_flag, a.status, a.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            d0 = tmem_base + (ac ^ 1u) * 256;
+            acc = 0;
+          }
           ok = mbar_wait(&full_bar[st], phase, abort_flag, a.status, a.wait_ns);
           if (!ok) break;
           tc_fence_after();
@@ -333,7 +354,8 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
           umma_commit_pair(&empty_bar[st]);
           if (++st == STAGES) { st = 0; phase ^= 1u; }
         }
-        if (ok) umma_commit_pair(&tmem_full[ac]);
+        if (ok) umma_commit_pair(&tmem_full[parts > 1 ? 0 : ac]);
+        if (parts > 1) ++joins;                                    // the last part's, waited for by the next tile
       }
       umma_commit_first(&sm.drain_bar);                            // all issued MMAs must finish before TMEM is released
       mbar_wait_drain(&sm.drain_bar, 0);
@@ -344,7 +366,7 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     const size_t ld = 2 * static_cast<size_t>(a.M);                // of the pre-activations and their gradients
     __nv_bfloat16* stg = sm.tile[warp - 2];
-    uint32_t it = 0;
+    uint32_t it = 0, joins = 0;
     int group = 0;
     for (int t = first; t < total; t += stride, ++it) {
       const SegTile ti = decode_tile(sm.sched, sp, t, group);
@@ -362,8 +384,37 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       }
       if (MODE == TRAIN_ROWS && mine && a.add)
         gr = load_tile_regs(a.add, static_cast<size_t>(a.M), ti.row0 + c0 * 32, ti.n_valid - c0 * 32, f0, lane);
-      if (!mbar_wait_warp(&tmem_full[ac], ac_ph, abort_flag, a.status, a.wait_ns)) break;
+      if (parts == 1 && !mbar_wait_warp(&tmem_full[ac], ac_ph, abort_flag, a.status, a.wait_ns)) break;
       tc_fence_after();
+      if (MODE == TRAIN_HIDDEN && parts > 1) {
+        // each further part is added to the first one's accumulator; the other is
+        // then free for the next part, or for the next tile's first
+        bool ok = true;
+        for (int p = 1; p < parts && ok; ++p, ++joins) {
+          ok = mbar_wait_warp(&tmem_full[0], joins & 1u, abort_flag, a.status, a.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+          auto free_other = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[0]);
+          };
+          if (c0 >= nchunk) free_other();
+          for (int c = c0; c < nchunk; c += cstep) {
+            float x[32], y[32];
+            tmem_ld32(lane_addr + (ac ^ 1u) * 256 + c * 32, y);
+            tmem_ld32(acc0 + c * 32, x);
+            tmem_ld_wait();
+            if (c + cstep >= nchunk) free_other();
+            uint32_t r[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(x[j] + y[j]);
+            tmem_st32(acc0 + c * 32, r);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+        if (!ok) break;
+      }
 #pragma unroll 1
       for (int s = 0; s < PASSES; ++s) {
         const int feat0 = f0 + s * 128;
@@ -463,7 +514,7 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[ac]);
+      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[parts > 1 ? 1 : ac]);
     }
   }
 
@@ -1039,6 +1090,7 @@ static cudaError_t train_gemm(const CUtensorMap& tmA, const HalfMaps& tmB, Train
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   a.n_mblk = (a.M + C::FEATS - 1) / C::FEATS;
+  a.parts = MODE == TRAIN_HIDDEN ? hidden_parts(a.K) : 1;
   const long long most = train_tiles(a.rows, a.groups, a.M, C::FEATS);
   const int pairs = num_sms / 2 < most ? num_sms / 2 : static_cast<int>(most);
   return launch_after(train_gemm_kernel<MODE, SUBS>, 2 * pairs, C::THREADS, smem, stream, tmA, tmB, a);

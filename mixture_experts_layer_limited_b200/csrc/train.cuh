@@ -20,6 +20,7 @@ struct TrainGemmArgs {
   const float* row_w = nullptr;       // hidden: [rows] or nullptr (= 1)
   __nv_bfloat16* d_gu = nullptr;      // hidden: [rows, 2I] out
   float* partial = nullptr;           // hidden: [I / 32, rows] out, partial sums of d_row_w
+  int32_t parts = 1;                  // hidden: parts of K (hidden_parts; set by the launcher)
   __nv_bfloat16* out = nullptr;       // rows: [rows, M]
   const __nv_bfloat16* add = nullptr; // rows: [rows, M] added to the product, or nullptr (may be `out`)
   int32_t* status = nullptr;
@@ -40,6 +41,12 @@ inline long long train_tiles(int rows, int groups, int M, int feats) {
 inline int train_subs(int rows, int groups, int K, int M, int num_sms) {
   return K > 512 && train_tiles(rows, groups, M, 512) >= num_sms / 2 ? 2 : 1;
 }
+// Parts of K that dh0 is summed in, which are added up in fp32 with rounding: the
+// tensor cores cut each of their sums towards zero, 16 terms at a time, so that
+// an unbroken sum of K terms comes out short by about 1e-9 K of itself, and
+// d_row_w, an fp32 output, with it (7168 terms: 7.9e-6 off). Parts of at most 896
+// terms leave 9e-7, for 1 to 2 % of a backward pass's time.
+inline int hidden_parts(int K) { return (K + 895) / 896; }
 cudaError_t launch_train_gemm(int mode, int subs, const CUtensorMap& tmA, const HalfMaps& tmB, const TrainGemmArgs& a,
                               int num_sms, cudaStream_t stream);
 cudaError_t launch_row_w_grad(int rows, int n, const float* partial, const int32_t* offsets, int groups, float* d_row_w,
