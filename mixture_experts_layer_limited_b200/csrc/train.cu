@@ -309,35 +309,30 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       const uint64_t ad0 = MODE == TRAIN_FORWARD ? sw128_desc(smem_u32(sm.stage[0])) : mn_desc(smem_u32(sm.stage[0]));
       const uint64_t bd0 = sw128_desc(smem_u32(sm.stage[0]) + C::A_BYTES);
       int st = 0;
-      uint32_t it = 0, phase = 0;
+      uint32_t phase = 0, freed = 0;                               // freed: parity of each accumulator's next wait
       bool ok = true;
-      int group = 0;
-      uint32_t joins = 0;                                          // parts joined so far
-      for (int t = first; t < total && ok; t += stride, ++it) {
+      int group = 0, cur = 0;
+      for (int t = first; t < total && ok; t += stride) {
         const SegTile ti = decode_tile(sm.sched, sp, t, group);
         const uint32_t idesc = make_idesc(1u, 256u, static_cast<uint32_t>(ti.N)) | (MODE == TRAIN_FORWARD ? 0u : kIdescAMn);
-        const uint32_t ac = it % ACCS, ac_ph = (it / ACCS) & 1u;
-        uint32_t d0 = tmem_base + ac * 256;
-        if (parts == 1)
-          ok = mbar_wait(&tmem_empty[ac], ac_ph ^ 1u, abort_flag, a.status, a.wait_ns);
-        else if (it > 0)                                           // the tile before has joined its last part
-          ok = mbar_wait(&tmem_empty[0], (joins - 1) & 1u, abort_flag, a.status, a.wait_ns);
+        const int keep = cur;
+        uint32_t d0 = tmem_base + cur * 256;
+        ok = mbar_wait(&tmem_empty[cur], ((freed >> cur) & 1u) ^ 1u, abort_flag, a.status, a.wait_ns);
         if (!ok) break;
+        freed ^= 1u << cur;
         tc_fence_after();
         uint32_t acc = 0;
-        int part = 0, part_end = nk / parts;
+        int part = 1, part_end = nk / parts;
         for (int kb = 0; kb < nk; ++kb) {
-          if (MODE == TRAIN_HIDDEN && parts > 1 && kb == part_end) {
-            // the next part, in the other accumulator, once that is free
-            if (part++ > 0) umma_commit_pair(&tmem_full[0]);
-            part_end = (part + 1) * nk / parts;
-            if (part > 1)
-              ok = mbar_wait(&tmem_empty[0], joins++ & 1u, abort_flag, a.status, a.wait_ns);
-            else if (it > 0)
-              ok = mbar_wait(&tmem_empty[1], (it - 1) & 1u, abort_flag, a.status, a.wait_ns);
+          if (MODE == TRAIN_HIDDEN && kb == part_end) {            // the next part, in another accumulator
+            umma_commit_pair(&tmem_full[cur]);
+            part_end = ++part * nk / parts;
+            cur = keep ^ 1;
+            ok = mbar_wait(&tmem_empty[cur], ((freed >> cur) & 1u) ^ 1u, abort_flag, a.status, a.wait_ns);
             if (!ok) break;
+            freed ^= 1u << cur;
             tc_fence_after();
-            d0 = tmem_base + (ac ^ 1u) * 256;
+            d0 = tmem_base + cur * 256;
             acc = 0;
           }
           ok = mbar_wait(&full_bar[st], phase, abort_flag, a.status, a.wait_ns);
@@ -354,8 +349,8 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
           umma_commit_pair(&empty_bar[st]);
           if (++st == STAGES) { st = 0; phase ^= 1u; }
         }
-        if (ok) umma_commit_pair(&tmem_full[parts > 1 ? 0 : ac]);
-        if (parts > 1) ++joins;                                    // the last part's, waited for by the next tile
+        if (ok) umma_commit_pair(&tmem_full[cur]);
+        cur = ACCS == 2 ? keep ^ 1 : 0;                            // the next tile's first part
       }
       umma_commit_first(&sm.drain_bar);                            // all issued MMAs must finish before TMEM is released
       mbar_wait_drain(&sm.drain_bar, 0);
@@ -366,13 +361,13 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     const size_t ld = 2 * static_cast<size_t>(a.M);                // of the pre-activations and their gradients
     __nv_bfloat16* stg = sm.tile[warp - 2];
-    uint32_t it = 0, joins = 0;
-    int group = 0;
-    for (int t = first; t < total; t += stride, ++it) {
+    uint32_t done = 0;                                             // parity of each accumulator's next wait
+    int group = 0, cur = 0;
+    for (int t = first; t < total; t += stride) {
       const SegTile ti = decode_tile(sm.sched, sp, t, group);
       const int nchunk = (ti.N + 31) / 32;
-      const uint32_t ac = it % ACCS, ac_ph = (it / ACCS) & 1u;
-      const uint32_t acc0 = lane_addr + ac * 256;
+      const int keep = cur;
+      const uint32_t acc0 = lane_addr + cur * 256;
       const int f0 = ti.mb * C::FEATS + C::FEATS / 2 * rank + 32 * q;
       constexpr int PASSES = MODE == TRAIN_FORWARD ? 1 : SUBS;     // sub-tiles of features
       // the first piece's other inputs, before the wait
@@ -384,25 +379,28 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       }
       if (MODE == TRAIN_ROWS && mine && a.add)
         gr = load_tile_regs(a.add, static_cast<size_t>(a.M), ti.row0 + c0 * 32, ti.n_valid - c0 * 32, f0, lane);
-      if (parts == 1 && !mbar_wait_warp(&tmem_full[ac], ac_ph, abort_flag, a.status, a.wait_ns)) break;
+      if (!mbar_wait_warp(&tmem_full[cur], (done >> cur) & 1u, abort_flag, a.status, a.wait_ns)) break;
+      done ^= 1u << cur;
+      cur = ACCS == 2 ? keep ^ 1 : 0;
       tc_fence_after();
       if (MODE == TRAIN_HIDDEN && parts > 1) {
-        // each further part is added to the first one's accumulator; the other is
-        // then free for the next part, or for the next tile's first
+        // each further part is added to the first one's accumulator; its own is then
+        // free for another part
         bool ok = true;
-        for (int p = 1; p < parts && ok; ++p, ++joins) {
-          ok = mbar_wait_warp(&tmem_full[0], joins & 1u, abort_flag, a.status, a.wait_ns);
+        for (int p = 1; p < parts; ++p) {
+          ok = mbar_wait_warp(&tmem_full[cur], (done >> cur) & 1u, abort_flag, a.status, a.wait_ns);
           if (!ok) break;
+          done ^= 1u << cur;
           tc_fence_after();
           auto free_other = [&] {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[0]);
+            if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[cur]);
           };
           if (c0 >= nchunk) free_other();
           for (int c = c0; c < nchunk; c += cstep) {
             float x[32], y[32];
-            tmem_ld32(lane_addr + (ac ^ 1u) * 256 + c * 32, y);
+            tmem_ld32(lane_addr + cur * 256 + c * 32, y);
             tmem_ld32(acc0 + c * 32, x);
             tmem_ld_wait();
             if (c + cstep >= nchunk) free_other();
@@ -514,7 +512,7 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[parts > 1 ? 1 : ac]);
+      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[keep]);
     }
   }
 
