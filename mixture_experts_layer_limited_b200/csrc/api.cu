@@ -121,11 +121,23 @@ moe_status make_train_weight_tmap(CUtensorMap* m, const void* w, int mode, int t
   return make_block_tmap(m, w, M, groups * K, 2 * subs);
 }
 
-// Token-row maps of a CTA pair: one box for each half tile of 16, 32, .. 128 rows.
-moe_status make_half_tmaps(HalfMaps* m, const void* ptr, uint64_t K, uint64_t rows) {
-  for (int i = 0; i < 8; ++i) {
-    moe_status s = make_tmap(&m->box[i], ptr, false, K, rows, 16 * (i + 1));
+// Token-row maps of a CTA pair: one box for each half tile of 16, 32, .. 128
+// rows that can occur: up to half of `rows`, or, with one segment of all rows
+// (no offsets), those of its full tiles and of its last one. The others are
+// copies, never loaded with.
+moe_status make_half_tmaps(HalfMaps* m, const void* ptr, uint64_t K, int32_t rows, const int32_t* offsets) {
+  const int32_t blocks = (rows + 255) / 256;
+  const int32_t full = ((rows + blocks - 1) / blocks + 31) / 32, last = (rows - (blocks - 1) * 32 * full + 31) / 32;
+  const int32_t most = blocks > 1 ? 8 : (rows + 31) / 32;
+  int32_t made = -1;
+  for (int32_t i = 0; i < 8; ++i) {
+    if (offsets ? i >= most : i + 1 != full && i + 1 != last) continue;
+    moe_status s = make_tmap(&m->box[i], ptr, false, K, static_cast<uint64_t>(rows), 16 * (i + 1));
     if (s != MOE_OK) return s;
+    if (made < 0)
+      for (int32_t j = 0; j < i; ++j) m->box[j] = m->box[i];
+    made = i;
+    for (int32_t j = i + 1; j < 8; ++j) m->box[j] = m->box[i];
   }
   return MOE_OK;
 }
@@ -584,7 +596,7 @@ moe_status moe_gate_up_swiglu_train(int32_t rows, int32_t H, const moe_ffn_weigh
   HalfMaps tmB;
   s = make_train_weight_tmap(&tmA, w->w13, TRAIN_FORWARD, w->tiled, w->groups, H, I, 2);
   if (s != MOE_OK) return s;
-  if ((s = make_half_tmaps(&tmB, a, H, rows)) != MOE_OK) return s;
+  if ((s = make_half_tmaps(&tmB, a, H, rows, offsets)) != MOE_OK) return s;
   TrainGemmArgs g;
   g.rows = rows;
   g.K = H;
@@ -945,7 +957,7 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
   HalfMaps tmB;
   s = make_train_weight_tmap(&tmA, w->w2, TRAIN_HIDDEN, w->tiled, w->groups, H, I, 1);
   if (s != MOE_OK) return s;
-  if ((s = make_half_tmaps(&tmB, d_out, H, rows)) != MOE_OK) return s;
+  if ((s = make_half_tmaps(&tmB, d_out, H, rows, offsets)) != MOE_OK) return s;
   TrainGemmArgs g;
   g.rows = rows;
   g.K = H;
@@ -971,7 +983,7 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
     const int subs = train_subs(rows, w->groups, 2 * I, H, nsm);
     s = make_train_weight_tmap(&tmA, w->w13, TRAIN_ROWS, w->tiled, w->groups, 2 * I, H, subs);
     if (s != MOE_OK) return s;
-    if ((s = make_half_tmaps(&tmB, d_gu, 2 * static_cast<uint64_t>(I), rows)) != MOE_OK) return s;
+    if ((s = make_half_tmaps(&tmB, d_gu, 2 * static_cast<uint64_t>(I), rows, offsets)) != MOE_OK) return s;
     g.K = 2 * I;
     g.M = H;
     g.out = static_cast<__nv_bfloat16*>(d_a);
@@ -1043,7 +1055,7 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
     HalfMaps tmB;
     const int subs = train_subs(T, 1, E, H, nsm);
     if ((s = make_train_weight_tmap(&tmA, gate_w, TRAIN_ROWS, 0, 1, E, H, subs)) != MOE_OK) return s;
-    if ((s = make_half_tmaps(&tmB, d_logits_bf16, E, T)) != MOE_OK) return s;
+    if ((s = make_half_tmaps(&tmB, d_logits_bf16, E, T, nullptr)) != MOE_OK) return s;
     TrainGemmArgs g;
     g.rows = T;
     g.K = E;
