@@ -446,7 +446,7 @@ moe_status launch_plan(const GemmPlan& p, int epi, cudaStream_t st, int nsm, con
 void mx_tile(int32_t rows, int32_t groups, MxGemmArgs* g) {
   const int32_t twice = 2 * ((rows + groups - 1) / groups);
   g->bn_max = twice <= 32 ? 32 : twice <= 64 ? 64 : 192;
-  g->stages = g->bn_max <= 64 ? 4 : 3;
+  g->stages = mx_stages(g->bn_max);
 }
 
 // A 4-bit weight's codes, w13 as [2 groups][I] rows (a gate block and the same

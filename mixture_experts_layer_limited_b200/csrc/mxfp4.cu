@@ -235,6 +235,11 @@ constexpr int kMxMaxStages = 4;
 constexpr uint32_t kMxA = 256 * 128;                                 // 256 weight rows x 256 values
 constexpr uint32_t kMxSfa = 2048;                                    // their scales
 __host__ __device__ constexpr uint32_t mx_stage_bytes(int bn) { return kMxA + kMxSfa + static_cast<uint32_t>(bn) * 128u; }
+// Dynamic shared memory of a launch, and of the largest one mx_tile gives.
+constexpr size_t mx_smem(int bn, int stages) { return static_cast<size_t>(stages) * mx_stage_bytes(bn) + 1024; }
+constexpr size_t kMxSmemMax = mx_smem(192, mx_stages(192));
+static_assert(mx_smem(32, mx_stages(32)) <= kMxSmemMax && mx_smem(64, mx_stages(64)) <= kMxSmemMax,
+              "192 rows a tile take the most shared memory");
 
 // Tiles as in the forward GEMMs: 256 weight rows (gate and up rows of 128
 // features, or 256 rows of w2) as the MMA's A, up to bn_max rows of a segment
@@ -545,11 +550,12 @@ mx_gemm_kernel(const __grid_constant__ MxMaps maps, const MxGemmArgs a) {
 
 // ---------------------------------------------------------------- launches
 cudaError_t launch_mx_gemm(bool gate_up, const MxMaps& maps, const MxGemmArgs& a, int grid, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(a.stages) * mx_stage_bytes(a.bn_max) + 1024;
   auto kern = gate_up ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // The limit belongs to the kernel, not to the launch: it is always the largest, so
+  // that another host thread's smaller call cannot lower it before this launch.
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMxSmemMax));
   if (e != cudaSuccess) return e;
-  return launch_after(kern, grid, kMxThreads, smem, stream, maps, a);
+  return launch_after(kern, grid, kMxThreads, mx_smem(a.bn_max, a.stages), stream, maps, a);
 }
 
 static dim3 mx_rows_grid(int rows, int K) {

@@ -5,13 +5,16 @@
 
 namespace moe {
 
+// Pipeline stages of a 4-bit GEMM with tiles of bn rows.
+constexpr int mx_stages(int bn) { return bn <= 64 ? 4 : 3; }
+
 // A grouped GEMM of 4-bit weights and rows (K values a row, packed two a byte).
 struct MxGemmArgs {
   int32_t rows = 0, K = 0, groups = 1;
   const int32_t* offsets = nullptr;    // [groups + 1] or nullptr (one segment)
   int32_t n_mblk = 0;                  // tiles of 256 weight rows per group
   int32_t bn_max = 32;                 // rows per tile at most: 32, 64 or 192
-  int32_t stages = 4;
+  int32_t stages = 4;                  // mx_stages(bn_max)
   const uint32_t* b_scale = nullptr;   // [K / 128, rows], four scale bytes each
   const float* row_w = nullptr;        // down: [rows] or nullptr
   void* out = nullptr;                 // gate/up: codes [rows, out_ld / 2]; down: bf16 [rows, out_ld]
