@@ -571,14 +571,25 @@ int gate_split(int T, int num_sms) {
   return 2;
 }
 
+// Dynamic shared memory of a launch for E experts: the ring, or what the CTAs of a
+// cluster exchange in its place.
+template <int SPLIT>
+constexpr size_t gate_smem(int E) {
+  const size_t ring = static_cast<size_t>(kRouteStages) * (128 * 128 + static_cast<size_t>(E) * 128);
+  const size_t recv = static_cast<size_t>(SPLIT - 1) * (kRouteRows / SPLIT) * (E + 4) * sizeof(float);
+  return (ring > recv ? ring : recv) + 1024;
+}
+
 template <int C, int SPLIT>
 cudaError_t launch_gate_route_split(const CUtensorMap& tmX, const CUtensorMap& tmG, const RouteArgs& r,
                                     uint32_t cols, cudaStream_t stream) {
-  const size_t ring = static_cast<size_t>(kRouteStages) * (128 * 128 + static_cast<size_t>(r.E) * 128);
-  const size_t recv = static_cast<size_t>(SPLIT - 1) * (kRouteRows / SPLIT) * (r.E + 4) * sizeof(float);
-  const size_t smem = (ring > recv ? ring : recv) + 1024;
+  const size_t smem = gate_smem<SPLIT>(r.E);
   auto kern = gate_route_kernel<C, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // The limit belongs to the kernel, not to the launch: it is always that of the
+  // most experts, so that another host thread's smaller call cannot lower it
+  // before this launch.
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(gate_smem<SPLIT>(256)));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(SPLIT * ((r.T + kRouteRows - 1) / kRouteRows));
