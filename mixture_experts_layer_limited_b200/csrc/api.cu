@@ -52,23 +52,39 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
+// Encodes a tensor map of `ptr` (no interleaving, zeros outside, every element).
+// The encoder wants the calling host thread's context, which a thread has only
+// from its first runtime call that needs one: where there is none yet, it gets
+// the current device's (allowed while a stream is captured).
+moe_status encode(CUtensorMap* m, CUtensorMapDataType type, uint32_t rank, const void* ptr, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  auto run = [&] {
+    return enc(m, type, rank, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = run();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(static_cast<int32_t>(e));
+    r = run();
+  }
+  return r == CUDA_SUCCESS ? MOE_OK : cuda_fail(1000 + static_cast<int32_t>(r));
+}
+
 // Row-major [outer, inner] matrix; box = 128 bytes of `inner` x box_rows rows,
 // 128-byte swizzle (the layout the tcgen05 smem descriptors expect).
 moe_status make_tmap(CUtensorMap* m, const void* ptr, bool one_byte, uint64_t inner, uint64_t outer,
                      uint32_t box_rows) {
-  EncodeTiledFn enc = encode_tiled();
-  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
   const uint64_t esize = one_byte ? 1 : 2;
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {inner * esize};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, one_byte ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                   const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
-  return MOE_OK;
+  return encode(m, one_byte ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box);
 }
 
 // Token-row maps of a grouped GEMM: bf16 rows are fetched with 256-, 128-,
@@ -86,17 +102,10 @@ moe_status make_token_tmaps(TokenMaps* m, const void* ptr, bool fp8, uint64_t K,
 // A 3-D bf16 tensor map with 128-byte swizzle; strides in bytes.
 moe_status make_tmap_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
                         uint32_t b1, uint32_t b2) {
-  EncodeTiledFn enc = encode_tiled();
-  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
   cuuint64_t dims[3] = {d0, d1, d2};
   cuuint64_t strides[2] = {s1, s2};
   cuuint32_t box[3] = {64, b1, b2};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
-  return MOE_OK;
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box);
 }
 
 // A row-major bf16 matrix [rows, cols] as [cols / 64] blocks of [rows, 64];
@@ -454,25 +463,17 @@ void mx_tile(int32_t rows, int32_t groups, MxGemmArgs* g) {
 // 2 x 128 rows of 128 bytes; its scales, 512 bytes per 128 x 128 values, in boxes
 // of the same 256 rows x 256 values.
 moe_status make_mx_weight_tmaps(MxMaps* m, bool gate_up, const moe_ffn_weights* w, int32_t H) {
-  EncodeTiledFn enc = encode_tiled();
-  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
   const uint64_t K = gate_up ? H : w->I, n = gate_up ? w->I : 128;
   const uint64_t blocks = gate_up ? 2 * static_cast<uint64_t>(w->groups) : static_cast<uint64_t>(w->groups) * (H / 128);
-  cuuint32_t estr[4] = {1, 1, 1, 1};
   cuuint64_t dims[3] = {K / 2, n, blocks}, strides[2] = {K / 2, K / 2 * n};
   cuuint32_t box[3] = {128, 128, 2};
-  CUresult r = enc(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(gate_up ? w->w13 : w->w2), dims, strides, box,
-                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
+  moe_status s = encode(&m->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, gate_up ? w->w13 : w->w2, dims, strides, box);
+  if (s != MOE_OK) return s;
   const uint64_t kb = K / 128, sn = gate_up ? w->I / 128 : blocks, sb = gate_up ? blocks : 1;
   cuuint64_t sdims[4] = {128, kb, sn, sb}, sstrides[3] = {512, 512 * kb, 512 * kb * sn};
   cuuint32_t sbox[4] = {128, 2, gate_up ? 1u : 2u, gate_up ? 2u : 1u};
-  r = enc(&m->w_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<float*>(gate_up ? w->w13_scale : w->w2_scale), sdims,
-          sstrides, sbox, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
-  return MOE_OK;
+  return encode(&m->w_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, gate_up ? w->w13_scale : w->w2_scale, sdims, sstrides, sbox,
+                CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // One 4-bit grouped GEMM (scales as moe_quantize_mxfp4_rows / _weights lay them out).
@@ -856,19 +857,11 @@ namespace {
 // [outer, inner] matrix stored through boxes of box_rows rows x 128 bytes,
 // bf16 or fp32.
 moe_status make_out_tmap(CUtensorMap* m, const void* ptr, bool f32, uint64_t inner, uint64_t outer, uint32_t box_rows) {
-  EncodeTiledFn enc = encode_tiled();
-  if (!enc) return cuda_fail(static_cast<int32_t>(cudaErrorNotSupported));
   const uint64_t esize = f32 ? 4 : 2;
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {inner * esize};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                   const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cuda_fail(1000 + static_cast<int32_t>(r));
-  return MOE_OK;
+  return encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
