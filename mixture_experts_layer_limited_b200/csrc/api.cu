@@ -304,6 +304,7 @@ struct Span {
   const void* ptr;
   size_t bytes;
 };
+Span offsets_span(const int32_t* offsets, int32_t groups) { return {offsets, (static_cast<size_t>(groups) + 1) * 4}; }
 bool overlap(const Span& p, const Span& q) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p.ptr), b = reinterpret_cast<uintptr_t>(q.ptr);
   return p.ptr && q.ptr && a < b + q.bytes && b < a + p.bytes;
@@ -589,7 +590,8 @@ moe_status moe_gate_up_swiglu_train(int32_t rows, int32_t H, const moe_ffn_weigh
   if (any_misaligned(offsets, h, gu)) return MOE_ERR_ALIGNMENT;
   const int I = w->I;
   const size_t r = static_cast<size_t>(rows);
-  if (!outputs_apart({{h, r * I * 2}, {gu, r * I * 4}}, {{a, r * H * 2}, {w->w13, static_cast<size_t>(w->groups) * I * H * 4}}))
+  if (!outputs_apart({{h, r * I * 2}, {gu, r * I * 4}}, {{a, r * H * 2}, {w->w13, static_cast<size_t>(w->groups) * I * H * 4},
+                                                         offsets_span(offsets, w->groups)}))
     return MOE_ERR_INVALID_ARG;
   int nsm = 0;
   if ((s = sm_count(&nsm)) != MOE_OK) return s;
@@ -933,7 +935,8 @@ moe_status moe_swiglu_ffn_backward(int32_t rows, int32_t H, const moe_ffn_weight
   const size_t esize = grad_dtype == MOE_F32 ? 4 : 2;
   // the products run beside one another: d_a in the place of a or d_out would be read after being written
   if (!outputs_apart({{d_a, r * H * 2}, {d_w13, weight * 2 * esize}, {d_w2, weight * esize}, {d_row_w, r * 4}, {workspace, ws.total}},
-                     {{a, r * H * 2}, {gu, r * I * 4}, {d_out, r * H * 2}, {row_w, r * 4}, {w->w13, weight * 4}, {w->w2, weight * 2}}))
+                     {{a, r * H * 2}, {gu, r * I * 4}, {d_out, r * H * 2}, {row_w, r * 4}, {w->w13, weight * 4}, {w->w2, weight * 2},
+                      offsets_span(offsets, w->groups)}))
     return MOE_ERR_INVALID_ARG;
   // output tiles of the weight gradients are counted in int32
   if (static_cast<long long>(w->groups) * (2 * I / 128) * (H / 256) > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED;
