@@ -449,7 +449,7 @@ MOE_API moe_status moe_gate_up_swiglu_gather(int32_t rows, int32_t H, const moe_
  *
  * Outputs (and the workspace) of these calls and of the 4-bit ones below that
  * overlap an input or one another are refused (MOE_ERR_INVALID_ARG), but for
- * dx_in == dx; moe_route_backward's are not checked.
+ * dx_in == dx and d_logits == logits.
  * ------------------------------------------------------------------------ */
 MOE_API moe_status moe_gate_up_swiglu_train(int32_t rows, int32_t H, const moe_ffn_weights* w, const void* a,
                               const int32_t* offsets, void* h, void* gu, int32_t* dev_status, void* stream);

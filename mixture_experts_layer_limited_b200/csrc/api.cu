@@ -1023,6 +1023,12 @@ moe_status moe_route_backward(int32_t T, int32_t E, int32_t k, moe_scoring scori
   if (k > 16 || E > 256 || E < 16 || E % 16 != 0) return MOE_ERR_UNSUPPORTED;
   if (static_cast<long long>(T) * k > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   if (any_misaligned(logits, topk_ids, d_topk_w, slot_to_row, d_logits, d_logits_bf16)) return MOE_ERR_ALIGNMENT;
+  const size_t values = static_cast<size_t>(T) * E, slots = static_cast<size_t>(T) * k * 4;
+  // a token's warp has read its logits before it writes: d_logits may take their place
+  const Span in{d_logits != logits ? logits : nullptr, values * 4};
+  if (!outputs_apart({{d_logits, values * 4}, {d_logits_bf16, values * 2}},
+                     {in, {topk_ids, slots}, {d_topk_w, slots}, {slot_to_row, slots}}))
+    return MOE_ERR_INVALID_ARG;
   return check_launch(launch_route_backward(T, E, k, scoring, norm_topk_prob ? 1 : 0, routed_scaling_factor, logits,
                                             topk_ids, d_topk_w, slot_to_row, d_logits, d_logits_bf16, dev_status,
                                             as_stream(stream)));
