@@ -990,11 +990,16 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
 // ========================================================================
 // w_j = scale * s_j (/ sum_i s_i if normalised), s the softmax or sigmoid
 // scores of the k chosen experts (the selection itself has no gradient):
-//   ds_j = scale * dw_j, normalised: scale / S * (dw_j - sum_i dw_i s_i / S)
-//   sigmoid: d_logit_e = s_e (1 - s_e) ds_e;  softmax: p_e (ds_e - sum_i p_i ds_i)
-// with ds_e = 0 for experts not chosen. One warp per token: lane j holds slot
-// j, lane l the experts l, l + 32, ... . Bound by its E logits' bytes: 8192
-// tokens x 256 experts (21 MB, from L2 in part) in 7.5 us.
+//   sigmoid: d_logit_j = scale dw_j s_j (1 - s_j);
+//   softmax: d_logit_e = p_e (ds_e - sum_i p_i ds_i), ds = scale dw, 0 for experts
+//     not chosen;
+//   normalised, with the shares r_j = s_j / S:  scale r_j (dw_j - sum_i dw_i r_i),
+//     for sigmoid times 1 - s_j; the other experts' are 0.
+// The shares come from scores scaled by e^-m, m the largest chosen logit (no more
+// than 0 for sigmoid), so that they are finite where the scores themselves leave
+// fp32's range (logits below -87). One warp per token: lane j holds slot j, lane l
+// the experts l, l + 32, ... . Bound by its E logits' bytes: 8192 tokens x 256
+// experts (21 MB, from L2 in part) in 7.5 us.
 __global__ void __launch_bounds__(256)
 route_backward_kernel(int T, int E, int k, int scoring, int norm, float scale, const float* logits,
                       const int32_t* ids, const float* d_w,
@@ -1026,52 +1031,65 @@ route_backward_kernel(int T, int E, int k, int scoring, int norm, float scale, c
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
   };
-  float p[PER];                                                    // softmax: this lane's probabilities
-  float top = 0.0f, inv = 0.0f;
-  if (scoring == MOE_SOFTMAX) {
-    top = -INFINITY;
+  auto all_max = [](float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+  };
+  // each slot's part of its expert's gradient, but for the sum over all experts
+  // that a softmax which is not renormalised adds
+  const bool full = scoring == MOE_SOFTMAX && !norm;
+  float p[PER];                                                    // full: this lane's probabilities
+  float part, dot = 0.0f;
+  if (full) {
+    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = lane + 32 * i;
       p[i] = e < E ? lg[e] : -INFINITY;
       top = fmaxf(top, p[i]);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    top = all_max(top);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       p[i] = expf(p[i] - top);
       sum += p[i];
     }
-    inv = 1.0f / all_sum(sum);
+    const float inv = 1.0f / all_sum(sum);
 #pragma unroll
     for (int i = 0; i < PER; ++i) p[i] *= inv;
+    part = id < 0 ? 0.0f : scale * dw;
+    dot = all_sum(id < 0 ? 0.0f : part * (expf(l_id - top) * inv));
+  } else if (norm) {
+    float m = all_max(id < 0 ? -INFINITY : l_id);
+    if (scoring == MOE_SIGMOID) m = fminf(m, 0.0f);
+    const float q = id < 0                    ? 0.0f
+                    : scoring == MOE_SOFTMAX  ? expf(l_id - m)
+                    : l_id > 0.0f             ? 1.0f / (1.0f + expf(-l_id))
+                                              : expf(l_id - m) / (1.0f + expf(l_id));
+    const float sum = all_sum(q), r = id < 0 ? 0.0f : q / sum;
+    const float mean = all_sum(dw * r);
+    part = id < 0 ? 0.0f : scale * r * (dw - mean);
+    if (scoring == MOE_SIGMOID) part *= 1.0f / (1.0f + expf(l_id));   // 1 - s without cancellation
+  } else {
+    const float s = 1.0f / (1.0f + expf(-l_id));
+    part = id < 0 ? 0.0f : scale * dw * (s * (1.0f / (1.0f + expf(l_id))));
   }
-  // scores of the chosen experts, and the gradient of each
-  const float s = id < 0 ? 0.0f : scoring == MOE_SOFTMAX ? expf(l_id - top) * inv : 1.0f / (1.0f + expf(-l_id));
-  float ds = id < 0 ? 0.0f : scale * dw;
-  if (norm) {
-    const float S = all_sum(s);
-    const float mean = all_sum(id < 0 ? 0.0f : dw * s) / S;
-    ds = id < 0 ? 0.0f : scale / S * (dw - mean);
-  }
-  if (scoring == MOE_SIGMOID) ds *= s * (1.0f / (1.0f + expf(l_id)));   // s (1 - s), both without cancellation
-  const float dot = scoring == MOE_SOFTMAX ? all_sum(ds * s) : 0.0f;
   float out[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) out[i] = 0.0f;
   for (int j = 0; j < k; ++j) {
     const int idj = __shfl_sync(0xffffffffu, id, j);
-    const float dsj = __shfl_sync(0xffffffffu, ds, j);
+    const float partj = __shfl_sync(0xffffffffu, part, j);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) out[i] += idj == lane + 32 * i ? dsj : 0.0f;
+    for (int i = 0; i < PER; ++i) out[i] += idj == lane + 32 * i ? partj : 0.0f;
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 32 * i;
     if (e < E) {
-      const float d = scoring == MOE_SOFTMAX ? p[i] * (out[i] - dot) : out[i];
+      const float d = full ? p[i] * (out[i] - dot) : out[i];
       d_logits[static_cast<size_t>(t) * E + e] = d;
       if (d_logits16) d_logits16[static_cast<size_t>(t) * E + e] = __float2bfloat16_rn(d);
     }
