@@ -422,10 +422,9 @@ MOE_API moe_status moe_gate_up_swiglu_gather(int32_t rows, int32_t H, const moe_
  *   dh0 and the activation's derivative are fp32; dg, du and row_w * h are
  *   rounded to bf16 once, as the operands of the second products; every sum
  *   is fp32 in a fixed order, so results do not vary from run to run. The tensor
- *   cores cut their sums towards zero every 16 terms: dh0 is summed in parts of
- *   at most 896 terms that are added with rounding (d_row_w within 1e-6 of its
- *   norm), the weight gradients over a segment's rows in one (fp32 ones short
- *   by about 1e-9 of themselves a row).
+ *   cores cut their sums towards zero every 16 terms: dh0, and fp32 weight
+ *   gradients over a segment's rows, are summed in parts of at most 896 terms
+ *   that are added with rounding (d_row_w within 1e-6 of its norm).
  *   A segment of offsets outside [0, rows] is cut to it and flagged
  *   MOE_DEVSTAT_BAD_EXPERT_ID in dev_status.
  *

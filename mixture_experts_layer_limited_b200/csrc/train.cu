@@ -658,7 +658,21 @@ __device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* o
   return w;
 }
 
-template <int SPLIT>
+// Parts that a tile's sum over so many blocks of rows is made in, in turn one
+// accumulator's and the other's. The tensor cores cut their sums towards zero every
+// 16 rows, always to the same side: equal-signed sums over 8192 rows came out
+// short by 2.5e-5 of themselves. fp32 gradients are summed in parts of at most 896
+// rows (hidden_parts), joined with rounding in TMEM; in bf16 ones it does not show.
+// What the joins cost on B200: one group of 8192 rows at V3 widths 830 -> 838 us of
+// the weight gradients' call, a gate's gradient (8192 tokens x 7168, 256 experts)
+// 33 -> 36 us.
+template <bool F32>
+__device__ __forceinline__ int wgrad_parts(int blocks) {
+  constexpr int kMost = 896 / WgradCfg::KB;
+  return F32 && blocks > kMost ? (blocks + kMost - 1) / kMost : 1;
+}
+
+template <int SPLIT, bool F32>
 __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(WgradCfg::THREADS, 1)
 wgrad_kernel(const __grid_constant__ WgradArgs a) {
   using C = WgradCfg;
@@ -725,7 +739,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
     uint8_t* row = box + lane * 128;
-    if (a.f32) {
+    if (F32) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         *reinterpret_cast<float4*>(row + ((i ^ (lane & 7)) << 4)) =
@@ -757,7 +771,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   };
-  const int cols = a.f32 ? 32 : 64;                                // columns of a box
+  const int cols = F32 ? 32 : 64;                                // columns of a box
 
   if (warp == 0) {
     if (lane == 0) {
@@ -808,51 +822,58 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       // their issue keeps only a few queued, and 700 cycles of bookkeeping a
       // block (512 of MMAs) cost a third of the rate.
       const uint64_t ad0 = mn_desc(smem_u32(sm.stage[0]));         // descriptor of stage 0's A
-      int st = 0;
-      uint32_t it = 0, full_par = 0, tail_par = 0;                 // parity of each stage's next wait, by barrier
+      int st = 0, cur = 0;                                         // stage; the next part's accumulator
+      uint32_t full_par = 0, tail_par = 0, freed = 0;              // parity of each stage's or accumulator's next wait
       bool ok = true;
-      for (WgradIter i(a, first, stride); i.t < total && ok; i.next(a, total), ++it) {
+      for (WgradIter i(a, first, stride); i.t < total && ok; i.next(a, total)) {
         const WgradTile w = wgrad_tile<SPLIT>(a, off, i, part);
         const uint32_t idesc = make_idesc(1u, 256u, w.N - w.n > 128 ? 256u : 128u) | kIdescAMn | kIdescBMn;
-        const uint32_t d0 = tmem_base + (it & 1u) * 256;
         const int even = w.kn / KB, rest = w.kn - even * KB;       // blocks of 64 rows, and the last one's rows
-        ok = mbar_wait(&tmem_empty[it & 1u], ((it >> 1) & 1u) ^ 1u, abort_flag, a.status, a.wait_ns);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t acc = 0;
-        for (int kb = 0; kb < even; ++kb) {
-          ok = mbar_wait(&full_bar[st], (full_par >> st) & 1u, abort_flag, a.status, a.wait_ns);
+        const int blocks = even + (rest > 0), parts = wgrad_parts<F32>(blocks), keep = cur;
+        for (int p = 1, kb = 0; p <= parts; ++p) {                 // the first part in one accumulator, further ones in the other
+          ok = mbar_wait(&tmem_empty[cur], ((freed >> cur) & 1u) ^ 1u, abort_flag, a.status, a.wait_ns);
           if (!ok) break;
+          freed ^= 1u << cur;
           tc_fence_after();
-          const uint64_t ad = ad0 + st * (C::STAGE_BYTES >> 4), bd = ad + (C::PAIR >> 4);
-#pragma unroll
-          for (int kk = 0; kk < KB / 16; ++kk) {                   // 2048 B a step, in the descriptors' 16-byte units
-            umma_bf16_pair(d0, ad + kk * 128, bd + kk * 128, idesc, acc);
-            acc = 1;
-          }
-          umma_commit_pair(&empty_bar[st], lead);
-          full_par ^= 1u << st;
-          if (++st == STAGES) st = 0;
-        }
-        if (ok && rest > 0) {
-          if (rest & 15) {
-            ok = mbar_wait(&sm.tail_done[st], (tail_par >> st) & 1u, abort_flag, a.status, a.wait_ns);
-            tail_par ^= 1u << st;
-          } else {
+          const uint32_t d0 = tmem_base + cur * 256;
+          const int end = p < parts ? p * blocks / parts : even;
+          uint32_t acc = 0;
+          for (; kb < end; ++kb) {
             ok = mbar_wait(&full_bar[st], (full_par >> st) & 1u, abort_flag, a.status, a.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = ad0 + st * (C::STAGE_BYTES >> 4), bd = ad + (C::PAIR >> 4);
+#pragma unroll
+            for (int kk = 0; kk < KB / 16; ++kk) {                 // 2048 B a step, in the descriptors' 16-byte units
+              umma_bf16_pair(d0, ad + kk * 128, bd + kk * 128, idesc, acc);
+              acc = 1;
+            }
+            umma_commit_pair(&empty_bar[st], lead);
             full_par ^= 1u << st;
+            if (++st == STAGES) st = 0;
+          }
+          if (ok && p == parts && rest > 0) {
+            if (rest & 15) {
+              ok = mbar_wait(&sm.tail_done[st], (tail_par >> st) & 1u, abort_flag, a.status, a.wait_ns);
+              tail_par ^= 1u << st;
+            } else {
+              ok = mbar_wait(&full_bar[st], (full_par >> st) & 1u, abort_flag, a.status, a.wait_ns);
+              full_par ^= 1u << st;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = ad0 + st * (C::STAGE_BYTES >> 4), bd = ad + (C::PAIR >> 4);
+            for (int kk = 0; kk < (rest + 15) / 16; ++kk) {
+              umma_bf16_pair(d0, ad + kk * 128, bd + kk * 128, idesc, acc);
+              acc = 1;
+            }
+            umma_commit_pair(&empty_bar[st], lead);
+            if (++st == STAGES) st = 0;
           }
           if (!ok) break;
-          tc_fence_after();
-          const uint64_t ad = ad0 + st * (C::STAGE_BYTES >> 4), bd = ad + (C::PAIR >> 4);
-          for (int kk = 0; kk < (rest + 15) / 16; ++kk) {
-            umma_bf16_pair(d0, ad + kk * 128, bd + kk * 128, idesc, acc);
-            acc = 1;
-          }
-          umma_commit_pair(&empty_bar[st], lead);
-          if (++st == STAGES) st = 0;
+          umma_commit_pair(&tmem_full[cur], lead);
+          cur = keep ^ 1;
         }
-        if (ok) umma_commit_pair(&tmem_full[it & 1u], lead);
       }
       // all issued MMAs must finish before TMEM is released
       umma_commit_first(&sm.drain_bar);
@@ -891,15 +912,45 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       for (int r = off[0] + blockIdx.x * 32 * EPIW + threadIdx.x - 64; r < hi; r += gridDim.x * 32 * EPIW)
         a.d_row_w[r] = sum_partials(a.partial, a.n_partial, a.rows, r);
     }
-    uint32_t it = 0;
-    for (WgradIter i(a, first, stride); i.t < total; i.next(a, total), ++it) {
+    int cur = 0;
+    uint32_t done = 0;                                             // parity of each accumulator's next wait
+    for (WgradIter i(a, first, stride); i.t < total; i.next(a, total)) {
       const WgradTile w = wgrad_tile<SPLIT>(a, off, i, part);
       const WgradProblem& pr = a.prob[w.p];
       const int width = w.N - w.n > 128 ? 256 : 128;
       const int m = w.m + 128 * rank + 32 * q;                     // this warp's 32 features of A
-      const uint32_t acc = lane_addr + (it & 1u) * 256;
-      if (!mbar_wait_warp(&tmem_full[it & 1u], (it >> 1) & 1u, abort_flag, a.status, a.wait_ns)) break;
+      const int keep = cur;
+      const uint32_t acc = lane_addr + keep * 256;
+      if (!mbar_wait_warp(&tmem_full[keep], (done >> keep) & 1u, abort_flag, a.status, a.wait_ns)) break;
+      done ^= 1u << keep;
+      cur = keep ^ 1;
       tc_fence_after();
+      // each further part is read, its accumulator handed back, and added to the first's
+      bool ok = true;
+      for (int p = wgrad_parts<F32>((w.kn + KB - 1) / KB); p > 1; --p) {
+        ok = mbar_wait_warp(&tmem_full[cur], (done >> cur) & 1u, abort_flag, a.status, a.wait_ns);
+        if (!ok) break;
+        done ^= 1u << cur;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 32 * half; c < width; c += 64) {              // this warp's columns
+          float x[32], y[32];
+          tmem_ld32(lane_addr + cur * 256 + c, y);
+          tmem_ld32(acc + c, x);
+          tmem_ld_wait();
+          if (c + 64 >= width) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[cur], lead);
+          }
+          uint32_t r[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(x[j] + y[j]);
+          tmem_st32(acc + c, r);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      }
+      if (!ok) break;
       if (SPLIT > 1) continue;                                     // one tile, summed over its pairs below
       const bool empty = w.kn == 0;
       // adding nothing needs no store, and rows past the matrix have none
@@ -909,7 +960,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
           float v[32], v2[32];
           if (!empty) {
             tmem_ld32(acc + c, v);
-            if (!a.f32) tmem_ld32(acc + c + 32, v2);
+            if (!F32) tmem_ld32(acc + c + 32, v2);
             tmem_ld_wait();
           } else {
 #pragma unroll
@@ -920,7 +971,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[it & 1u], lead);
+      if (lane == 0) mbar_arrive_first_relaxed(&tmem_empty[keep], lead);
     }
     if (SPLIT == 1 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
@@ -959,16 +1010,16 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
       for (int c = half * cols; c < CW; c += 2 * cols) {
         float v[32], v2[32];
         tmem_ld32(acc + part * CW + c, v);
-        if (!a.f32) tmem_ld32(acc + part * CW + c + 32, v2);
+        if (!F32) tmem_ld32(acc + part * CW + c + 32, v2);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           if (!w.kn) v[j] = 0.0f;
-          if (!w.kn || a.f32) v2[j] = 0.0f;
+          if (!w.kn || F32) v2[j] = 0.0f;
           for (int o = 0; o < SPLIT - 1; ++o) {
             const float* f = got + (o * CW + c + j) * 128 + 32 * q + lane;
             v[j] += f[0];
-            if (!a.f32) v2[j] += f[32 * 128];
+            if (!F32) v2[j] += f[32 * 128];
           }
         }
         store(w, part * CW + c, v, v2);
@@ -1134,16 +1185,17 @@ cudaError_t launch_route_backward(int T, int E, int k, int scoring, int norm, fl
                       slot_to_row, d_logits, static_cast<__nv_bfloat16*>(d_logits16), status);
 }
 
-template <int SPLIT>
+template <int SPLIT, bool F32>
 static cudaError_t wgrad(const WgradArgs& a, int clusters, cudaStream_t stream) {
   constexpr size_t smem = sizeof(WgradSmem);
   static_assert(smem <= 232448, "wgrad_kernel's shared memory exceeds an SM's");
-  cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<SPLIT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_after(wgrad_kernel<SPLIT>, 2 * SPLIT * clusters, WgradCfg::THREADS, smem, stream, a);
+  return launch_after(wgrad_kernel<SPLIT, F32>, 2 * SPLIT * clusters, WgradCfg::THREADS, smem, stream, a);
 }
-cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
+template <bool F32>
+static cudaError_t wgrad_any(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   int tiles = 0;
   bool wide = true;                                    // whole tiles of 256 columns
   for (int p = 0; p < a.n_prob; ++p) {
@@ -1158,9 +1210,12 @@ cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   // eight: 16 tiles of 2048 rows in two turns of the latter 25 us) and 256 rows a
   // pair and segment.
   const int rows = a.rows / a.groups;
-  if (wide && 4 * tiles <= room && tiles <= num_sms * 15 / 148 && rows >= 4 * 256) return wgrad<4>(a, tiles, stream);
-  if (wide && 2 * tiles <= room && tiles <= num_sms * 33 / 148 && rows >= 2 * 256) return wgrad<2>(a, tiles, stream);
-  return wgrad<1>(a, room < tiles ? room : tiles, stream);
+  if (wide && 4 * tiles <= room && tiles <= num_sms * 15 / 148 && rows >= 4 * 256) return wgrad<4, F32>(a, tiles, stream);
+  if (wide && 2 * tiles <= room && tiles <= num_sms * 33 / 148 && rows >= 2 * 256) return wgrad<2, F32>(a, tiles, stream);
+  return wgrad<1, F32>(a, room < tiles ? room : tiles, stream);
+}
+cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
+  return a.f32 ? wgrad_any<true>(a, num_sms, stream) : wgrad_any<false>(a, num_sms, stream);
 }
 
 }  // namespace moe
