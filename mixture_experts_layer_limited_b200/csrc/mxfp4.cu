@@ -365,7 +365,7 @@ mx_gemm_kernel(const __grid_constant__ MxMaps maps, const MxGemmArgs a) {
           for (int c = 0; c < 8; ++c) {
             const int r = c * 32 + lane;                             // rows behind the tile's: scale 1, not used
             x[8 * kh + c] = kk < k128 && r < ti.n_valid
-                                ? __ldg(a.b_scale + static_cast<size_t>(kk) * a.rows + ti.row0 + r) : 0x7f7f7f7fu;
+                                ? a.b_scale[static_cast<size_t>(kk) * a.rows + ti.row0 + r] : 0x7f7f7f7fu;
           }
         }
       };
@@ -448,7 +448,7 @@ mx_gemm_kernel(const __grid_constant__ MxMaps maps, const MxGemmArgs a) {
       float* ws = ts + 512;                                          // down: the rows' weights, behind the store tile
       if (!GATE_UP) {
         for (int r = lane; r < 32 * nchunk; r += 32)
-          ws[r] = r < ti.n_valid ? (a.row_w ? __ldg(a.row_w + ti.row0 + r) : 1.0f) : 0.0f;
+          ws[r] = r < ti.n_valid ? (a.row_w ? a.row_w[ti.row0 + r] : 1.0f) : 0.0f;
         __syncwarp();
       }
       if (!mbar_wait_warp(&tmem_full, it & 1u, &abort_flag, a.status, a.wait_ns)) break;

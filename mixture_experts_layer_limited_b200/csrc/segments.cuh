@@ -266,7 +266,7 @@ __device__ __forceinline__ void frag_row_values(const float* src, int n_rows, in
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int r = frag_row(lane, k >> 1, k & 1);
-    w[k] = r < n_rows ? (src ? __ldg(src + r) : none) : 0.0f;
+    w[k] = r < n_rows ? (src ? src[r] : none) : 0.0f;
   }
 }
 
