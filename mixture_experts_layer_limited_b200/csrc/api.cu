@@ -1055,8 +1055,7 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
   if (dx) {                                            // dx = dx_in + d_logits gate
     CUtensorMap tmA;
     HalfMaps tmB;
-    const int subs = train_subs(T, 1, E, H, nsm);
-    if ((s = make_train_weight_tmap(&tmA, gate_w, TRAIN_ROWS, 0, 1, E, H, subs)) != MOE_OK) return s;
+    if ((s = make_train_weight_tmap(&tmA, gate_w, TRAIN_ROWS, 0, 1, E, H, 1)) != MOE_OK) return s;
     if ((s = make_half_tmaps(&tmB, d_logits_bf16, E, T, nullptr)) != MOE_OK) return s;
     TrainGemmArgs g;
     g.rows = T;
@@ -1064,10 +1063,10 @@ moe_status moe_gate_backward(int32_t T, int32_t H, int32_t E, const void* d_logi
     g.M = H;
     g.out = static_cast<__nv_bfloat16*>(dx);
     g.add = static_cast<const __nv_bfloat16*>(dx_in);
-    rows_tiles = tiles_in_int(train_tiles(T, 1, H, subs * 256));
+    rows_tiles = tiles_in_int(train_tiles(T, 1, H, 256));
     g.status = dev_status;
     g.wait_ns = wait_limit();
-    if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, subs, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
+    if ((s = check_launch(launch_train_gemm(TRAIN_ROWS, 1, tmA, tmB, g, nsm, st))) != MOE_OK) return s;
   }
   if (d_gate) {                                        // d_gate = d_logits^T x
     WgradArgs q{};

@@ -13,7 +13,6 @@ constexpr int kMaxGroups = 512;
 struct SegTile {
   int g, mb, row0, n_valid, N;
   int ntb;              // token blocks of this segment
-  int tb;               // this tile's token block in the segment
 };
 
 // Token blocks per rasterisation chunk: inside a segment, tiles run in chunks
@@ -131,7 +130,6 @@ __device__ __forceinline__ SegTile decode_in_segment(const SegProblem& a, int g,
   ti.mb = quick_div(r, c_tb);
   const int tb = chunk * kTbChunk + (r - ti.mb * c_tb);
   ti.ntb = ntb;
-  ti.tb = tb;
   ti.row0 = seg0 + tb * bn;
   ti.n_valid = min(bn, n - tb * bn);
   ti.N = (ti.n_valid + a.unit - 1) & ~(a.unit - 1);
@@ -142,20 +140,6 @@ __device__ __forceinline__ SegTile decode_in_segment(const SegProblem& a, int g,
 __device__ __forceinline__ SegTile decode_tile(const SegSched& s, const SegProblem& a, int t, int& g) {
   while (t >= s.tile_start[g + 1]) ++g;
   return decode_in_segment(a, g, s.seg_start[g], s.seg_start[g + 1] - s.seg_start[g], t - s.tile_start[g]);
-}
-
-// Token rows of one stage (a multiple of 16, at most 256) are fetched with at
-// most one box of each size 256, 128, 64, 32, 16: the binary digits of
-// rows / 16. Returns rows loaded.
-template <typename LoadFn>
-__device__ __forceinline__ int load_token_rows(int rows, LoadFn&& load) {
-  int off = 0;
-#pragma unroll
-  for (int i = 0; i < kTokBoxes; ++i) {
-    const int box = 256 >> i;
-    if (rows - off >= box) { load(i, off); off += box; }
-  }
-  return off;
 }
 
 // ---- 32 features x 32 rows of an accumulator, as the tensor cores' fragments

@@ -379,7 +379,7 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         gr = load_tile_regs(a.gu, ld, ti.row0 + c0 * 32, ti.n_valid - c0 * 32, f0, lane);
         ur = load_tile_regs(a.gu, ld, ti.row0 + c0 * 32, ti.n_valid - c0 * 32, a.M + f0, lane);
       }
-      if (MODE == TRAIN_ROWS && mine && a.add)
+      if (MODE == TRAIN_ROWS && SUBS == 1 && mine && a.add)
         gr = load_tile_regs(a.add, static_cast<size_t>(a.M), ti.row0 + c0 * 32, ti.n_valid - c0 * 32, f0, lane);
       if (!mbar_wait_warp(&tmem_full[cur], (done >> cur) & 1u, abort_flag, a.status, a.wait_ns)) break;
       done ^= 1u << cur;
@@ -492,14 +492,11 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             if (r < n_rows) a.partial[static_cast<size_t>(feat0 / 32) * a.rows + row0 + r] = sum[0];
           } else {
             tmem_ld_wait();
-            if (a.add) {
+            if (SUBS == 1 && a.add) {                              // only a short K has rows to add to
               uint32_t add[16];
               spread_frag(stg, gr, lane, add);
               if (c + cstep < nchunk)
                 gr = load_tile_regs(a.add, static_cast<size_t>(a.M), row1, n_rows1, feat0, lane);
-              else if (s + 1 < PASSES && feat0 + 128 < a.M)
-                gr = load_tile_regs(a.add, static_cast<size_t>(a.M), ti.row0 + c0 * 32, ti.n_valid - c0 * 32, feat0 + 128,
-                                    lane);
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 const float2 o = unpack_bf16(add[k]);

@@ -22,7 +22,7 @@ struct TrainGemmArgs {
   float* partial = nullptr;           // hidden: [I / 32, rows] out, partial sums of d_row_w
   int32_t parts = 1;                  // hidden: parts of K (hidden_parts; set by the launcher)
   __nv_bfloat16* out = nullptr;       // rows: [rows, M]
-  const __nv_bfloat16* add = nullptr; // rows: [rows, M] added to the product, or nullptr (may be `out`)
+  const __nv_bfloat16* add = nullptr; // rows, one sub-tile: [rows, M] added to the product, or nullptr (may be `out`)
   int32_t* status = nullptr;
   uint64_t wait_ns = kDefaultWaitLimitNs;
 };
