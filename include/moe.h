@@ -252,7 +252,9 @@ MOE_API moe_status moe_permute_static_ws(int32_t T, int32_t k, int32_t E, int32_
  *             [rows, H/128] when w->dtype == MOE_E4M3; MOE_MXFP4: codes
  *             [rows, H/2] and scales from moe_quantize_mxfp4_rows.
  *   offsets   [groups+1] device int32 segment starts (from moe_permute), or
- *             NULL: one group covering all rows (groups must be 1).
+ *             NULL: one group covering all rows (groups must be 1). A start
+ *             outside [0, rows] is cut to it, one below an earlier start to
+ *             that one, and MOE_DEVSTAT_BAD_EXPERT_ID flagged in dev_status.
  *   row_w     [rows] fp32 per-row output weight fused into the epilogue of
  *             the second GEMM, or NULL (= 1).
  *   h_ws      [rows, I] intermediate: bf16, or e4m3 codes with h_scale_ws
@@ -425,8 +427,7 @@ MOE_API moe_status moe_gate_up_swiglu_gather(int32_t rows, int32_t H, const moe_
  *   cores cut their sums towards zero every 16 terms: dh0, and fp32 weight
  *   gradients over a segment's rows, are summed in parts of at most 896 terms
  *   that are added with rounding (d_row_w within 1e-6 of its norm).
- *   A segment of offsets outside [0, rows] is cut to it and flagged
- *   MOE_DEVSTAT_BAD_EXPERT_ID in dev_status.
+ *   offsets that fall or leave [0, rows]: as in the forward.
  *
  * moe_route_backward: gradient of the routing weights w.r.t. the logits:
  *     w_j = scale s_j (/ sum_i s_i with norm_topk_prob), s the softmax or

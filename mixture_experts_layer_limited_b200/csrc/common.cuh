@@ -324,6 +324,10 @@ __device__ __forceinline__ bool wait_count(const int32_t* count, int32_t target,
   }
 }
 
+// SiLU(g) = g * sigmoid(g). Fast division: for g < -88 the exponential
+// overflows to inf and the quotient is the correct limit (-0).
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
 // E4M3 code of v (round to nearest even, saturate to +-448).
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));

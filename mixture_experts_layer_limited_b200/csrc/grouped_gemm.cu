@@ -39,120 +39,15 @@
 // The E4M3 variant accumulates each 128-wide K block separately in a TMEM
 // ring and promotes it with the fp32 block scales on the CUDA cores, since
 // the weight scale is per 128x128 block and the activation scale per 1x128.
-#include "kernels.cuh"
+#include "schedule.cuh"
 
 namespace moe {
 
-constexpr int kMaxGroups = 512;
 constexpr int kThreads = 192;
-
-struct TileInfo {
-  int g, mb, row0, n_valid, N;
-  int ntb;              // token blocks of this segment
-  int tb;               // this tile's token block in the segment
-};
-
-// Token blocks per rasterisation chunk: inside a segment, tiles run in chunks
-// of up to kTbChunk token blocks x all weight blocks, token block innermost,
-// so CTAs running side by side share the weight block (HBM once, then L2)
-// and the chunk's token blocks (L2).
-constexpr int kTbChunk = 8;
 
 // Pipeline stages of 64 K: bf16 (64 KB each), E4M3.
 constexpr int kBf16Stages = 3;
 constexpr int kE4m3Stages = 4;
-
-// Per-CTA copy of the tile schedule: tb_start[g] = first token block of
-// group g (over all groups), tile_start[g] = its first tile (tb_start[g] x
-// the problem's weight blocks).
-struct Sched {
-  int tile_start[kMaxGroups + 1];
-  int seg_start[kMaxGroups + 1];
-  int tb_start[kMaxGroups + 1];
-};
-
-__device__ __forceinline__ int tiles_of(int n, int bn_max, int n_mblk) {
-  return n <= 0 ? 0 : ((n + bn_max - 1) / bn_max) * n_mblk;
-}
-
-// Warp-cooperative build of the schedule (called by one warp).
-__device__ void build_schedule(Sched& s, const GemmArgs& a, int lane) {
-  int carry = 0;
-  for (int base = 0; base < a.groups; base += 32) {
-    const int g = base + lane;
-    int st = 0, n = 0;
-    if (g < a.groups) {
-      if (a.offsets) {
-        st = a.offsets[g];
-        n = a.offsets[g + 1] - st;
-      } else {
-        st = 0;
-        n = a.rows;
-      }
-    }
-    int t = (g < a.groups) ? tiles_of(n, a.bn_max, 1) : 0;   // token blocks
-    int incl = t;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      int v = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += v;
-    }
-    if (g < a.groups) {
-      s.tb_start[g] = carry + incl - t;
-      s.tile_start[g] = (carry + incl - t) * a.n_mblk;
-      s.seg_start[g] = st;
-    }
-    carry += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  if (lane == 0) {
-    s.tb_start[a.groups] = carry;
-    s.tile_start[a.groups] = carry * a.n_mblk;
-    s.seg_start[a.groups] = a.offsets ? a.offsets[a.groups] : a.rows;
-  }
-}
-
-// Tile `local` of a segment of n rows starting at row seg0 (group g).
-__device__ __forceinline__ TileInfo decode_in_segment(const GemmArgs& a, int g, int seg0, int n, int local) {
-  TileInfo ti;
-  ti.g = g;
-  const int ntb = (n + a.bn_max - 1) / a.bn_max;
-  const int bn = ((((n + ntb - 1) / ntb) + 15) / 16) * 16;
-  const int chunk_tiles = kTbChunk * a.n_mblk;
-  const int chunk = local / chunk_tiles;
-  const int r = local - chunk * chunk_tiles;
-  const int c_tb = min(kTbChunk, ntb - chunk * kTbChunk);   // token blocks in this chunk
-  ti.mb = r / c_tb;
-  const int tb = chunk * kTbChunk + (r - ti.mb * c_tb);
-  ti.ntb = ntb;
-  ti.tb = tb;
-  ti.row0 = seg0 + tb * bn;
-  ti.n_valid = min(bn, n - tb * bn);
-  ti.N = ((ti.n_valid + 15) / 16) * 16;
-  return ti;
-}
-
-__device__ __forceinline__ TileInfo decode_tile(const Sched& s, const GemmArgs& a, int t) {
-  int lo = 0, hi = a.groups - 1;   // last g with tile_start[g] <= t
-  while (lo < hi) {
-    int mid = (lo + hi + 1) >> 1;
-    if (s.tile_start[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  return decode_in_segment(a, lo, s.seg_start[lo], s.seg_start[lo + 1] - s.seg_start[lo],
-                           t - s.tile_start[lo]);
-}
-
-// Tile t of problem a over the schedule's segments when a's weight blocks per
-// group differ from those the schedule was built with (its token blocks are
-// the same: same offsets and bn_max).
-__device__ __forceinline__ TileInfo decode_tile_nb(const Sched& s, const GemmArgs& a, int t) {
-  int lo = 0, hi = a.groups - 1;   // last g with tb_start[g] * n_mblk <= t
-  while (lo < hi) {
-    int mid = (lo + hi + 1) >> 1;
-    if (s.tb_start[mid] * a.n_mblk <= t) lo = mid; else hi = mid - 1;
-  }
-  return decode_in_segment(a, lo, s.seg_start[lo], s.seg_start[lo + 1] - s.seg_start[lo],
-                           t - s.tb_start[lo] * a.n_mblk);
-}
 
 // The weight rows of K block kb of a tile. Row-major weights: sub-tiles at
 // rows a_row0 and a_row1 (128 rows each), or one 256-row box at a_row0, read
@@ -207,10 +102,6 @@ __device__ __forceinline__ void store_tile(__nv_bfloat16* stage, const float (&v
   __syncwarp();
 }
 
-// SiLU(g) = g * sigmoid(g). Fast division: for g < -88 the exponential
-// overflows to inf and the quotient is the correct limit (-0).
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
-
 // ========================================================================
 // BF16 kernel
 // ========================================================================
@@ -235,7 +126,7 @@ grouped_gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA,
   constexpr int KB = 64;                           // K elements per stage (128 B)
   constexpr uint32_t A_SUB_BYTES = 128 * 128;      // one 128-row sub-tile
   extern __shared__ __align__(1024) uint8_t dsmem[];
-  __shared__ Sched sched;
+  __shared__ SegSched sched;
   __shared__ __align__(16) __nv_bfloat16 stage_out[EPIW][32 * 32];
   __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
   __shared__ uint64_t tmem_full, tmem_empty, drain_bar;
@@ -284,7 +175,7 @@ grouped_gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA,
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_s;
   const int total2 = TWO ? tiles_of(a2.rows, a.bn_max, a2.n_mblk) : 0;
-  const int total = total2 + sched.tile_start[a.groups];
+  const int total = total2 + total_tiles(sched, a);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -295,7 +186,7 @@ grouped_gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA,
       uint32_t phase = 0;
       for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x) {
         const bool sh = TWO && t < total2;
-        const TileInfo ti = sh ? decode_in_segment(a2, 0, 0, a2.rows, t) : decode_tile(sched, a, t - total2);
+        const SegTile ti = sh ? decode_in_segment(a2, 0, 0, a2.rows, t) : decode_tile(sched, a, t - total2);
         const int nk = (sh ? a2.K : a.K) / KB;
         const CUtensorMap* mA = sh ? &tmA2 : &tmA;
         const TokenMaps* mB = sh ? &tmB2 : &tmB;
@@ -337,7 +228,7 @@ grouped_gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA,
     uint32_t phase = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok && !abort_flag; t += gridDim.x) {
-      const TileInfo ti = decode_tile(sched, a, t);
+      const SegTile ti = decode_tile(sched, a, t);
       int srow[32];                                    // source rows of this thread's token rows
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -377,7 +268,7 @@ grouped_gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA,
       uint32_t phase = 0, it = 0;
       for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x, ++it) {
         const bool sh = TWO && t < total2;
-        const TileInfo ti = sh ? decode_in_segment(a2, 0, 0, a2.rows, t) : decode_tile(sched, a, t - total2);
+        const SegTile ti = sh ? decode_in_segment(a2, 0, 0, a2.rows, t) : decode_tile(sched, a, t - total2);
         const int nk = (sh ? a2.K : a.K) / KB;
         const uint32_t idesc = make_idesc(1u, 128u, static_cast<uint32_t>(ti.N));
         const uint32_t d0 = tmem_base;
@@ -416,7 +307,7 @@ grouped_gemm_bf16_kernel(const __grid_constant__ CUtensorMap tmA,
     uint32_t it = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
       const bool sh = TWO && t < total2;
-      const TileInfo ti = sh ? decode_in_segment(a2, 0, 0, a2.rows, t) : decode_tile(sched, a, t - total2);
+      const SegTile ti = sh ? decode_in_segment(a2, 0, 0, a2.rows, t) : decode_tile(sched, a, t - total2);
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(sh ? a2.out : a.out);
       const size_t out_ld = sh ? a2.out_ld : a.out_ld;
       const int feat_stride = sh ? a2.feat_stride : a.feat_stride;
@@ -526,7 +417,7 @@ grouped_ffn_bf16_kernel(const __grid_constant__ FfnArgs f) {
   constexpr uint32_t A_SUB_BYTES = 128 * 128;
   constexpr uint32_t sub_cols = 256u;
   extern __shared__ __align__(1024) uint8_t dsmem[];
-  __shared__ Sched sched;
+  __shared__ SegSched sched;
   __shared__ __align__(16) __nv_bfloat16 stage_out[EPIW][32 * 32];
   __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
   __shared__ uint64_t tmem_full, tmem_empty, drain_bar, tile_bar;
@@ -580,7 +471,7 @@ grouped_ffn_bf16_kernel(const __grid_constant__ FfnArgs f) {
   const int first3 = first2 + tiles_of(f.g[2].rows, f.g[2].bn_max, f.g[2].n_mblk);
   const int total = first3 + tb_routed * f.g[3].n_mblk;
   // problem of tile t, its tile info and its token block's counter
-  auto locate = [&](int t, int& p, TileInfo& ti) -> int {
+  auto locate = [&](int t, int& p, SegTile& ti) -> int {
     p = t < first1 ? 0 : t < first2 ? 1 : t < first3 ? 2 : 3;
     const int base = p == 0 ? 0 : p == 1 ? first1 : p == 2 ? first2 : first3;
     const GemmArgs& g = f.g[p];
@@ -588,7 +479,7 @@ grouped_ffn_bf16_kernel(const __grid_constant__ FfnArgs f) {
       ti = decode_in_segment(g, 0, 0, g.rows, t - base);
       return f.shared_base + ti.tb;
     }
-    ti = decode_tile_nb(sched, g, t - base);
+    ti = decode_tile(sched, g, t - base);
     return sched.tb_start[ti.g] + ti.tb;
   };
 
@@ -603,7 +494,7 @@ grouped_ffn_bf16_kernel(const __grid_constant__ FfnArgs f) {
       while (next < total && !abort_flag) {
         const int t = next;
         int p;
-        TileInfo ti;
+        SegTile ti;
         const int idx = locate(t, p, ti);
         const GemmArgs& g = f.g[p];
         if (p >= 2) {                                  // h rows of this token block stored and visible
@@ -661,7 +552,7 @@ grouped_ffn_bf16_kernel(const __grid_constant__ FfnArgs f) {
         mbar_arrive(&tile_bar);
         if (t < 0) break;
         int p;
-        TileInfo ti;
+        SegTile ti;
         locate(t, p, ti);
         const int nk = f.g[p].K / KB;
         const uint32_t idesc = make_idesc(1u, 128u, static_cast<uint32_t>(ti.N));
@@ -705,7 +596,7 @@ grouped_ffn_bf16_kernel(const __grid_constant__ FfnArgs f) {
       const int t = acc_tile;
       if (t < 0) break;
       int p;
-      TileInfo ti;
+      SegTile ti;
       const int idx = locate(t, p, ti);
       const GemmArgs& g = f.g[p];
       __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(g.out);
@@ -785,7 +676,7 @@ grouped_gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmA,
   constexpr uint32_t B_BYTES = kF8Bn * 128;
   constexpr uint32_t STAGE_BYTES = 2 * A_SUB_BYTES + B_BYTES;
   extern __shared__ __align__(1024) uint8_t dsmem[];
-  __shared__ Sched sched;
+  __shared__ SegSched sched;
   __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
   __shared__ uint64_t part_full[kF8Slots], part_empty[kF8Slots];
   __shared__ uint64_t drain_bar, epi_bar;
@@ -828,7 +719,7 @@ grouped_gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmA,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_s;
-  const int total = sched.tile_start[a.groups];
+  const int total = total_tiles(sched, a);
   const int nk = a.K / KB;
 
   if (warp == 0) {
@@ -839,7 +730,7 @@ grouped_gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmA,
       int stage = 0;
       uint32_t phase = 0;
       for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x) {
-        const TileInfo ti = decode_tile(sched, a, t);
+        const SegTile ti = decode_tile(sched, a, t);
         const int a_row0 = ti.g * a.a_rows_per_group + ti.mb * a.mblk_stride;
         const int a_row1 = a_row0 + a.sub1_off;
         const uint32_t bytes = 2 * A_SUB_BYTES + B_BYTES;
@@ -867,7 +758,7 @@ grouped_gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmA,
       uint32_t phase = 0;
       uint32_t kbg = 0;   // K blocks issued so far (TMEM ring position)
       for (int t = blockIdx.x; t < total && !abort_flag; t += gridDim.x) {
-        const TileInfo ti = decode_tile(sched, a, t);
+        const SegTile ti = decode_tile(sched, a, t);
         const uint32_t idesc = make_idesc(0u, 128u, static_cast<uint32_t>(ti.N));
         bool ok = true;
         for (int kb = 0; kb < nk; ++kb, ++kbg) {
@@ -910,7 +801,7 @@ grouped_gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tmA,
       return r;
     };
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const TileInfo ti = decode_tile(sched, a, t);
+      const SegTile ti = decode_tile(sched, a, t);
       // activation scales of this tile's rows -> smem
       if (!epi_sync()) break;
       for (int i = et; i < kF8Bn * nk; i += 128) {

@@ -314,7 +314,7 @@ mx_gemm_kernel(const __grid_constant__ MxMaps maps, const MxGemmArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_s;
-  const int total = sched.tile_start[a.groups];
+  const int total = total_tiles(sched, sp);
   const int k128 = a.K / 128;                                        // blocks of 128 values
   const int nk = (k128 + 1) / 2;                                     // stages per tile
 

@@ -248,7 +248,7 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   cluster_sync();                                                  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
   const uint32_t tmem_base = sm.tmem_base;
-  const int total = sm.sched.tile_start[a.groups];
+  const int total = total_tiles(sm.sched, sp);
   const int nk = (a.K + KB - 1) / KB;
   const int parts = MODE == TRAIN_HIDDEN ? a.parts : 1;
 
@@ -634,8 +634,8 @@ struct WgradIter {
 };
 struct WgradTile { int p, g, m, n, N, k0, kn; };
 
-// `off`: the segments' starts in shared memory, cut to the rows there are; part
-// `part` of SPLIT of the segment's blocks of rows.
+// `off`: the segments' starts in shared memory (cut_starts); part `part` of SPLIT
+// of the segment's blocks of rows.
 template <int SPLIT>
 __device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* off, const WgradIter& i, int part) {
   WgradTile w;
@@ -645,7 +645,7 @@ __device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* o
   w.n = i.ni * 256;
   w.N = a.prob[i.p].N;
   w.k0 = off[w.g];
-  w.kn = max(off[w.g + 1] - w.k0, 0);                    // a segment that ends before it starts has no rows
+  w.kn = off[w.g + 1] - w.k0;
   if (SPLIT > 1) {
     const int blocks = (w.kn + WgradCfg::KB - 1) / WgradCfg::KB;
     const int from = part * blocks / SPLIT * WgradCfg::KB, to = (part + 1) * blocks / SPLIT * WgradCfg::KB;
@@ -720,10 +720,16 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
     griddep_wait();
     griddep_launch_dependents();
   }
-  for (int i = threadIdx.x; i <= a.groups; i += blockDim.x)
-    sm.off[i] = a.offsets ? min(max(a.offsets[i], 0), a.rows) : i * a.rows;
+  bool lie = true;
+  for (int i = threadIdx.x; i <= a.groups; i += blockDim.x) {
+    sm.off[i] = a.offsets ? a.offsets[i] : i * a.rows;
+    lie = lie && (i == a.groups || !a.offsets || seg_lies(sm.off[i], a.offsets[i + 1], a.rows));
+  }
   tc_fence_before();
-  __syncthreads();
+  if (!__syncthreads_and(lie)) {
+    if (warp == 2) cut_starts(sm.off, a.offsets, a.groups, a.rows, a.status, lane);
+    __syncthreads();
+  }
   cluster_sync();                                                  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
   const uint32_t tmem_base = sm.tmem_base;
