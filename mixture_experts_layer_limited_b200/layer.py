@@ -387,9 +387,10 @@ class MoELayer:
             raise ValueError("forward_train needs a bf16 layer without gather")
         if T > self.T_max or x.dtype != torch.bfloat16 or not x.is_contiguous():
             raise ValueError("x: contiguous bf16 rows, at most T_max of them")
-        if x.untyped_storage().data_ptr() == self.y.untyped_storage().data_ptr():
-            raise ValueError("x is this layer's output buffer, which its forward overwrites")
         t, R = self._train_buffers(), T * s.k
+        for own, by in ((self.y, "forward"), (t["dx"], "backward")):
+            if x.untyped_storage().data_ptr() == own.untyped_storage().data_ptr():
+                raise ValueError(f"x is this layer's output buffer, which its {by} overwrites")
         self.route(x)
         self.permute(x, T)
         N.moe_gate_up_swiglu_train(R, s.H, self.w13, s.E, s.I, self.x_perm[:R], self.offsets, self.h[:R], t["gu"][:R],
