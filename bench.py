@@ -33,7 +33,7 @@ sys.path.insert(0, ROOT)
 
 METRIC = "MoE-layer fwd tokens/s and achieved TFLOP/s vs B200 peak at V3 shape"
 PROFILE_DIR = os.path.join(ROOT, "profiles")      # *_traffic.txt: DRAM bytes of one launch per workload
-GEMM_SOURCES = ["grouped_gemm.cu", "common.cuh", "kernels.cuh"]
+GEMM_SOURCES = ["grouped_gemm.cu", "schedule.cuh", "common.cuh", "kernels.cuh"]
 
 
 def parse_args():
