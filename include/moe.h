@@ -426,7 +426,9 @@ MOE_API moe_status moe_gate_up_swiglu_gather(int32_t rows, int32_t H, const moe_
  *   is fp32 in a fixed order, so results do not vary from run to run. The tensor
  *   cores cut their sums towards zero every 16 terms: dh0, and fp32 weight
  *   gradients over a segment's rows, are summed in parts of at most 896 terms
- *   that are added with rounding (d_row_w within 1e-6 of its norm).
+ *   that are added with rounding: short by at most 1.6e-6 of its norm a part
+ *   (d_row_w of random rows: 8.7e-7 measured; fp32 weight gradients over 8192
+ *   rows: 7.9e-7).
  *   offsets that fall or leave [0, rows]: as in the forward.
  *
  * moe_route_backward: gradient of the routing weights w.r.t. the logits:

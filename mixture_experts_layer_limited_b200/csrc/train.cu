@@ -451,7 +451,11 @@ train_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
               ur = load_tile_regs(a.gu, ld, row1, n_rows1, a.M + feat0, lane);
             }
             tmem_ld_wait();
-            // g <- dg, u <- du, p <- row_w h; sums of h dh0 over this thread's four features of each row
+            // g <- dg, u <- du, p <- row_w h; sums of h dh0 over this thread's four features of each row.
+            // dg, du and row_w h are computed in fp32 and rounded to bf16 here, once: they are the
+            // second products' operands, and those multiply them with bf16 weights and rows (an
+            // instruction takes one type). With it the gradients are 2.4e-3 of their norm from the
+            // 64-bit value; fp32 throughout and rounded at the end, 1.7e-3.
             float sum[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
@@ -657,8 +661,8 @@ __device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs& a, const int* o
 
 // Parts that a tile's sum over so many blocks of rows is made in, in turn one
 // accumulator's and the other's. The tensor cores cut their sums towards zero every
-// 16 rows, always to the same side: equal-signed sums over 8192 rows came out
-// short by 2.5e-5 of themselves. fp32 gradients are summed in parts of at most 896
+// 16 rows, always to the same side: sums over 8192 rows came out short by 2.9e-5
+// of themselves with equal signs, 9.1e-6 with random ones. fp32 gradients are summed in parts of at most 896
 // rows (hidden_parts), joined with rounding in TMEM; in bf16 ones it does not show.
 // What the joins cost on B200: one group of 8192 rows at V3 widths 830 -> 838 us of
 // the weight gradients' call, a gate's gradient (8192 tokens x 7168, 256 experts)
@@ -1051,7 +1055,10 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
 //     for sigmoid times 1 - s_j; the other experts' are 0.
 // The shares come from scores scaled by e^-m, m the largest chosen logit (no more
 // than 0 for sigmoid), so that they are finite where the scores themselves leave
-// fp32's range (logits below -87). One warp per token: lane j holds slot j, lane l
+// fp32's range (logits below -87). The bf16 copy of d_logits is for the gate's
+// products, whose operands are of one type: one rounding more for dx and d_gate
+// (2.3e-3 of their norm from the 64-bit value instead of 1.7e-3), none for the fp32
+// d_logits. One warp per token: lane j holds slot j, lane l
 // the experts l, l + 32, ... . Bound by its E logits' bytes: 8192 tokens x 256
 // experts (21 MB, from L2 in part) in 7.5 us.
 __global__ void __launch_bounds__(256)

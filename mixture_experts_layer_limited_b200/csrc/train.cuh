@@ -42,10 +42,11 @@ inline int train_subs(int rows, int groups, int K, int M, int num_sms) {
   return K > 512 && train_tiles(rows, groups, M, 512) >= num_sms / 2 ? 2 : 1;
 }
 // Parts of K that dh0 is summed in, which are added up in fp32 with rounding: the
-// tensor cores cut each of their sums towards zero, 16 terms at a time, so that
-// an unbroken sum of K terms comes out short by about 1e-9 K of itself, and
-// d_row_w, an fp32 output, with it (7168 terms: 7.9e-6 off). Parts of at most 896
-// terms leave 9e-7, for 1 to 2 % of a backward pass's time.
+// tensor cores cut each of their sums towards zero, 16 terms at a time, and
+// d_row_w, an fp32 output, is short with them (7168 terms of random rows in one
+// sum: 7.9e-6 of its norm; equal signs lose up to three times as much). Parts of
+// at most 896 terms lose 1.6e-6 at most, 9e-7 measured, for 1 to 2 % of a backward
+// pass's time.
 inline int hidden_parts(int K) { return (K + 895) / 896; }
 cudaError_t launch_train_gemm(int mode, int subs, const CUtensorMap& tmA, const HalfMaps& tmB, const TrainGemmArgs& a,
                               int num_sms, cudaStream_t stream);
