@@ -72,3 +72,25 @@ def test_fp32_gradients_of_segments_in_parts(counts, H, I, accumulate):
             assert bool(((o[k].to(F64) - i.to(F64) - ref[k]).abs() <= tol).all()), k
     else:
         T._check(o, c, off, H, I)
+
+
+def test_wait_limit_in_fp32_parts():
+    """The wait limit in weight gradients that come in parts: the call gives up,
+    flags it, and the same call with the default limit gives what it gave before."""
+    H, I = 512, 384
+    c, off, R, E = T._case([4000, 0, 1000], H, I, seed=79)
+    before = T._backward(c, off, R, E, H, I, f32=True)
+    offs = torch.tensor(off, dtype=torch.int32, device=DEV)
+    ws = torch.empty(N.moe_swiglu_ffn_backward_workspace_size(R, I), dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    d13, d2 = torch.zeros_like(before["d_w13"]), torch.zeros_like(before["d_w2"])
+    N.moe_set_wait_limit_ns(5)
+    try:
+        N.moe_swiglu_ffn_backward(R, H, c["w13"], c["w2"], E, I, c["a"], c["gu"], c["d_out"], offs, c["row_w"], None, d13, d2,
+                                  None, ws, grad_dtype=N.MOE_F32, dev_status=status)
+        assert N.moe_read_device_status(status) == N.MOE_DEVSTAT_TIMEOUT
+    finally:
+        N.moe_set_wait_limit_ns(0)
+    after = T._backward(c, off, R, E, H, I, f32=True)
+    for k in before:
+        assert torch.equal(before[k], after[k])
