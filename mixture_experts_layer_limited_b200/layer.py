@@ -189,6 +189,7 @@ class MoELayer:
         (x_perm codes + scales, and the unpermuted codes xq / xs the shared
         expert reads). 4-bit layers quantise the rows as they are gathered."""
         s = self.spec
+        self._train_x = None                   # these rows replace forward_train()'s
         R = T * s.k
         if self.fp8:
             N.moe_permute(T, s.k, s.E, s.H, self.ids[:T], self.topk_w[:T], x, N.MOE_BF16, None,

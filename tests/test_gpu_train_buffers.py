@@ -38,3 +38,13 @@ def test_own_buffers_as_the_gradient(name):
     assert torch.equal(layer.backward(dx, want), got)
     for k in want:
         assert torch.equal(grads[k], want[k])
+
+
+def test_a_permutation_ends_forward_train_s_claim():
+    """permute() on its own (a stage of the forward) writes over the rows that
+    backward() needs."""
+    inp, layer = _layer(_cfg("tiny"))
+    layer.forward_train(inp.x)
+    layer.permute((inp.x * 2).contiguous(), inp.x.shape[0])
+    with pytest.raises(ValueError, match="without forward_train"):
+        layer.backward(inp.x, layer.grad_buffers())
