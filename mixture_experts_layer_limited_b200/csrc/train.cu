@@ -1123,16 +1123,18 @@ route_backward_kernel(int T, int E, int k, int scoring, int norm, float scale, c
     part = id < 0 ? 0.0f : scale * dw;
     dot = all_sum(id < 0 ? 0.0f : part * (expf(l_id - top) * inv));
   } else if (norm) {
+    const bool sig = scoring == MOE_SIGMOID;
     float m = all_max(id < 0 ? -INFINITY : l_id);
-    if (scoring == MOE_SIGMOID) m = fminf(m, 0.0f);
-    const float q = id < 0                    ? 0.0f
-                    : scoring == MOE_SOFTMAX  ? expf(l_id - m)
-                    : l_id > 0.0f             ? 1.0f / (1.0f + expf(-l_id))
-                                              : expf(l_id - m) / (1.0f + expf(l_id));
+    if (sig) m = fminf(m, 0.0f);
+    // sigmoid, with t = e^-|l|: s is 1 / (1 + t) above 0 and e^l / (1 + t) below,
+    // 1 - s is t / (1 + t) and 1 / (1 + t): neither cancels
+    const float t = sig ? expf(-fabsf(l_id)) : 0.0f, inv = 1.0f / (1.0f + t);
+    const bool up = sig && l_id > 0.0f;
+    const float q = id < 0 ? 0.0f : up ? inv : expf(l_id - m) * inv;
     const float sum = all_sum(q), r = id < 0 ? 0.0f : q / sum;
     const float mean = all_sum(dw * r);
     part = id < 0 ? 0.0f : scale * r * (dw - mean);
-    if (scoring == MOE_SIGMOID) part *= 1.0f / (1.0f + expf(l_id));   // 1 - s without cancellation
+    if (sig) part *= up ? t * inv : inv;
   } else {
     const float s = 1.0f / (1.0f + expf(-l_id));
     part = id < 0 ? 0.0f : scale * dw * (s * (1.0f / (1.0f + expf(l_id))));
