@@ -170,8 +170,9 @@ __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f
 // on each of 32 experts, and at V2-Lite's layer: one CTA per tile of 256 x 256
 // with one accumulator 365 / 445 and 374 / 253 us; SUBS = 1 303 / 568 and
 // 233 / 317 us (dh0 in one sum; in parts 290 to 360 and 260); SUBS = 2 for d_a
-// 480 and 293. The forward at V3 widths: 460 us at full clock, 580 under the
-// power cap (1050 and 830 TFLOP/s).
+// 480 and 293. The forward at V3 widths: 440 us in a burst of 30 ms (1100
+// TFLOP/s), 507 to 600 in a long loop, where the power cap holds the clock near
+// 1.2 GHz.
 //   forward: sub-tile 0 holds the gate rows of the CTA's 128 features, sub-tile
 //   1 their up rows, so that one thread has both.
 // Warp 0 loads, warp 1 of the first CTA issues the MMAs, twelve epilogue warps:
@@ -1060,7 +1061,7 @@ wgrad_kernel(const __grid_constant__ WgradArgs a) {
 // (2.3e-3 of their norm from the 64-bit value instead of 1.7e-3), none for the fp32
 // d_logits. One warp per token: lane j holds slot j, lane l
 // the experts l, l + 32, ... . Bound by its E logits' bytes: 8192 tokens x 256
-// experts (21 MB, from L2 in part) in 7.5 us.
+// experts (21 MB, from L2 in part) in 5.5 to 6.8 us as a graph.
 __global__ void __launch_bounds__(256)
 route_backward_kernel(int T, int E, int k, int scoring, int norm, float scale, const float* logits,
                       const int32_t* ids, const float* d_w,
