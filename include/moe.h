@@ -34,6 +34,8 @@
  *     runs out ORs a code into it (MOE_DEVSTAT_*) and the kernel returns.
  *     Read it with moe_read_device_status. After a wait runs out, the
  *     kernel's outputs are incomplete, but the CUDA context stays usable.
+ *   - Several host threads may call at once, each with its own outputs and
+ *     workspaces (moe_permute_static_ws excepted: it has one array).
  *   - No C++ exception crosses this interface.
  */
 #ifndef MOE_B200_MOE_H
