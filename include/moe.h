@@ -66,7 +66,7 @@ typedef int32_t moe_status;
 #define MOE_ERR_DEVICE_TIMEOUT 6  /* device status: a bounded wait ran out    */
 
 /* bits ORed into *dev_status by kernels */
-#define MOE_DEVSTAT_BAD_EXPERT_ID 0x1 /* a topk id outside [0, E)            */
+#define MOE_DEVSTAT_BAD_EXPERT_ID 0x1 /* an expert id, row or offset out of range */
 #define MOE_DEVSTAT_TIMEOUT       0x2 /* an mbarrier wait exceeded its limit */
 
 typedef int32_t moe_dtype;
